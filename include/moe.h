@@ -375,6 +375,112 @@ moe_status_t moe_forward(const moe_cfg_t* cfg, int32_t T, const void* x_bf16, in
                          const void* w2, const void* w2_scale, void* out_bf16, int64_t ld_out,
                          void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Dense MXFP4: quantisation along either axis of a matrix, and products of
+ * quantised matrices, for what surrounds the experts (a shared expert, the
+ * projections) and for training.  Quantised matrices here are row-major codes
+ * u8 [rows, Cp/2] with E8M0 scales u8 [rows, Cp/32], Cp = cols rounded up to
+ * 128, grouped along the row: the layout of moe_quant_act.  The codes past
+ * `cols` have to be zero, as the quantisers write them.  All sizes may be
+ * zero; each is at most 2^24, and a (padded) matrix at most 2^40 elements.
+ * Alignment: codes 16 bytes, scales 4, workspaces 16, other matrices their
+ * element's size; else MOE_ERR_ALIGN.  Row strides are in elements and not
+ * below the row's length.  Outputs must not overlap inputs or workspaces. */
+
+/* Quantises in [rows, cols] (MOE_DTYPE_BF16 or _F32) along its rows into q_row
+ * [rows, Cp/2] and s_row [rows, Cp/32], and / or along its columns (that is,
+ * the rows of its transpose) into q_col [cols, Rp/2] and s_col [cols, Rp/32],
+ * Rp = rows rounded up to 128, from one read.  A pair may be NULL.  Per group
+ * of 32: b = clamp(floor(log2 amax) - 2 + 127, 0, 254) (0 when amax = 0),
+ * codes = RNE_E2M1(clamp(v / 2^(b-127), +-6)), as moe_quant_act.  A group
+ * that holds an infinity or a NaN gets scale 255, the format's NaN, and zero
+ * codes, so that a product over it is NaN. */
+moe_status_t moe_mxfp4_quant(const void* in, int32_t in_dtype, int32_t rows, int32_t cols, int64_t ld_in,
+                             void* q_row, void* s_row, void* q_col, void* s_col, void* stream);
+
+/* out[r, c] = E2M1(code) * 2^(scale - 127) for c < cols (NaN where the scale
+ * is 255), exact in both output types (an MXFP4 value past their range, which
+ * no quantiser here writes, becomes an infinity). */
+moe_status_t moe_mxfp4_dequant(const void* q, const void* scales, int32_t rows, int32_t cols, int32_t out_dtype,
+                               void* out, int64_t ld_out, void* stream);
+
+/* out[m, n] = sum over k of deq(a)[m, k] deq(b)[n, k], a [M, K] and b [N, K]
+ * quantised along K; fp32 sums, in an order fixed by the sizes alone, rounded
+ * once where out is bf16.  accumulate != 0 (fp32 out only) adds to out.
+ * K = 0: sums of nothing.  ws: at least moe_mxfp4_matmul_bytes(M, N, K) bytes
+ * (0, and ws may be NULL, where the sum over K is not split; also 0 for
+ * invalid sizes). */
+size_t moe_mxfp4_matmul_bytes(int32_t M, int32_t N, int32_t K);
+moe_status_t moe_mxfp4_matmul(int32_t M, int32_t N, int32_t K, const void* a, const void* a_scale, const void* b,
+                              const void* b_scale, int32_t out_dtype, void* out, int64_t ld_out, int32_t accumulate,
+                              void* ws, size_t ws_bytes, void* stream);
+
+/* A linear layer with MXFP4 weights: out[M, N] = Q(x) deq(w)^T, x [M, K]
+ * (bf16 or f32) quantised along its rows by this call, w [N, K] quantised
+ * along K.  The results are those of moe_mxfp4_quant and moe_mxfp4_matmul up
+ * to the order of the fp32 sums.  ws: at least moe_mxfp4_linear_bytes. */
+size_t moe_mxfp4_linear_bytes(int32_t M, int32_t N, int32_t K);
+moe_status_t moe_mxfp4_linear(int32_t M, int32_t N, int32_t K, const void* x, int32_t x_dtype, int64_t ld_x,
+                              const void* w, const void* w_scale, int32_t out_dtype, void* out, int64_t ld_out,
+                              void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradients from dy [M, N] (bf16 or f32), which this call quantises along
+ * both axes; the quantisations themselves pass gradients straight through:
+ *   dx[M, K] = Q_n(dy) W, w_col [K, N]: W quantised along N (q_col of W);
+ *   dw[N, K] = Q_m(dy)^T X, x_col [K, M]: x quantised along M (q_col of x),
+ *              fp32, added to dw where accumulate != 0.
+ * dx or dw may be NULL (then so may w_col or x_col).  ws: at least
+ * moe_mxfp4_linear_bwd_bytes. */
+size_t moe_mxfp4_linear_bwd_bytes(int32_t M, int32_t N, int32_t K);
+moe_status_t moe_mxfp4_linear_bwd(int32_t M, int32_t N, int32_t K, const void* dy, int32_t dy_dtype, int64_t ld_dy,
+                                  const void* x_col, const void* x_col_scale, const void* w_col,
+                                  const void* w_col_scale, int32_t dx_dtype, void* dx, int64_t ld_dx, float* dw,
+                                  int64_t ld_dw, int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Training the router.  T tokens' logits f32 [T, E] (E <= 1024) and the ids
+ * int32 [T, k] that moe_route_topk chose (k <= 16).  seq_offsets: int32
+ * [num_seqs + 1] on the device, non-decreasing within [0, T] (sequence s is
+ * the rows seq_offsets[s] .. seq_offsets[s+1]; empty ones are allowed; values
+ * outside [0, T] are clamped, and decreasing ones leave the results
+ * unspecified), or NULL for one sequence of all T rows (num_seqs = 1);
+ * num_seqs <= 65536.  token_mask: u8 [T], 0 for a token to leave out (its
+ * logits and ids are not used), or NULL.  A token is valid if it lies in a
+ * sequence, is not masked and has a logit above -inf; -inf excludes an
+ * expert.  Ids outside [0, E) are skipped.  Pointers 4-byte aligned, ws 16.
+ *
+ * moe_balance_loss, with p = softmax(logits) over the E experts:
+ *   n_s valid tokens of sequence s, N all of them, S' sequences with n_s > 0;
+ *   counts[s, e] pairs of valid tokens of s routed to e (int32 [num_seqs, E]);
+ *   loss[0] = 1/S' sum_s sum_e (E counts[s,e] / (k n_s)) (1/n_s sum_t p[t,e])
+ *             (1 for a uniform router with even counts);
+ *   loss[1] = 1/N sum_t lse[t]^2;  both 0 without valid tokens;
+ *   seq_tokens int32 [num_seqs + 2]: the n_s, then N and S';
+ *   lse f32 [T]: log sum_e exp(logits[t, e]), 0 for tokens that are not valid.
+ * fp32 sums in a fixed order: repeated calls give the same bits.  ws: at least
+ * moe_balance_bytes(T, E, num_seqs) bytes (0 for invalid sizes).  A valid
+ * token with a NaN or +inf logit makes the losses NaN.
+ *
+ * moe_router_bwd: d_logits f32 [T, E] (written whole; 0 for tokens that are
+ * not valid) from the gradients d_loss f32 [2] (device) of the two losses and
+ * d_weights f32 [T, k] of moe_route_topk's weights; either may be NULL.  The
+ * counts are constants:
+ *   a[e] = d_loss[0] E counts[s,e] / (S' k n_s^2)
+ *   d_logits[t, e] = p_e (a_e - sum p a) + d_loss[1] 2/N lse[t] p_e
+ *     + sum over j with ids[t,j] = e of w_j (dw_j - sum_i w_i dw_i)
+ * lse, counts and seq_tokens as moe_balance_loss wrote them for the same
+ * mask and sequences (NULL without d_loss); ids and weights may be NULL
+ * without d_weights. */
+size_t moe_balance_bytes(int32_t T, int32_t E, int32_t num_seqs);
+moe_status_t moe_balance_loss(const float* logits, const int32_t* ids, int32_t T, int32_t E, int32_t top_k,
+                              const uint8_t* token_mask, const int32_t* seq_offsets, int32_t num_seqs, float* loss,
+                              int32_t* counts, int32_t* seq_tokens, float* lse, void* ws, size_t ws_bytes,
+                              void* stream);
+moe_status_t moe_router_bwd(const float* logits, const int32_t* ids, const float* weights, const float* d_weights,
+                            int32_t T, int32_t E, int32_t top_k, const uint8_t* token_mask,
+                            const int32_t* seq_offsets, int32_t num_seqs, const float* lse, const int32_t* counts,
+                            const int32_t* seq_tokens, const float* d_loss, float* d_logits, void* stream);
+
 /* Diagnostic (not part of the layer): one 16x16 output tile C = A . B^T over
  * K = 128 from e4m3 codes, computed as one K block of the grouped GEMMs:
  * kind 0 with one FP8 MFMA (16x16x128, unit scales; GEMM2's instruction),

@@ -100,6 +100,18 @@ _SIGS = {
     "moe_diag_mfma_tile": (ctypes.c_int, [_I32, _P, _P, _P, _P]),
     "moe_diag_mfma_rate": (ctypes.c_int, [_I32, _I32, _P, _P]),
     "moe_diag_stream_read": (ctypes.c_int, [_P, _I64, _P, _P]),
+    "moe_mxfp4_quant": (ctypes.c_int, [_P, _I32, _I32, _I32, _I64, _P, _P, _P, _P, _P]),
+    "moe_mxfp4_dequant": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, _P, _I64, _P]),
+    "moe_mxfp4_matmul_bytes": (_SZ, [_I32, _I32, _I32]),
+    "moe_mxfp4_matmul": (ctypes.c_int, [_I32, _I32, _I32, _P, _P, _P, _P, _I32, _P, _I64, _I32, _P, _SZ, _P]),
+    "moe_mxfp4_linear_bytes": (_SZ, [_I32, _I32, _I32]),
+    "moe_mxfp4_linear": (ctypes.c_int, [_I32, _I32, _I32, _P, _I32, _I64, _P, _P, _I32, _P, _I64, _P, _SZ, _P]),
+    "moe_mxfp4_linear_bwd_bytes": (_SZ, [_I32, _I32, _I32]),
+    "moe_mxfp4_linear_bwd": (ctypes.c_int, [_I32, _I32, _I32, _P, _I32, _I64, _P, _P, _P, _P, _I32, _P, _I64, _P, _I64,
+                                            _I32, _P, _SZ, _P]),
+    "moe_balance_bytes": (_SZ, [_I32, _I32, _I32]),
+    "moe_balance_loss": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_router_bwd": (ctypes.c_int, [_P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _P, _P, _P, _P]),
     "moe_decode_supported": (_I32, [_CFGP, _I32]),
     "moe_decode_gemm1_swiglu": (ctypes.c_int, [_CFGP, _I32, _P, _P, _P, _P, _P, _P, _P]),
     "moe_decode_gemm2_combine": (ctypes.c_int, [_CFGP, _I32, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _P]),
@@ -451,6 +463,301 @@ def moe_forward_noalloc(cfg: MoeCfg, x: torch.Tensor, logits: torch.Tensor, w13,
                                     _dev(out, torch.bfloat16, "out", contiguous=False), out.stride(0),
                                     _stream(stream)), "moe_forward_noalloc")
     return out
+
+
+# ---- dense MXFP4 -------------------------------------------------------------
+
+_FLOAT_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+
+
+def _padded(n: int) -> int:
+    return (n + 127) // 128 * 128
+
+
+def _float_dtype(dtype, name: str) -> int:
+    code = _FLOAT_DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bf16 or f32")
+    return code
+
+
+def _matrix(t: torch.Tensor, name: str) -> int:
+    """The dtype code of a bf16 or f32 device matrix with unit column stride
+    (and rows that do not overlap)."""
+    code = _float_dtype(t.dtype, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return code
+
+
+def _ld(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _codes(q: torch.Tensor, s: torch.Tensor, rows: int, cols: int, device, name: str):
+    """Checks MXFP4 codes and scales of a [rows, cols] matrix."""
+    cp = _padded(cols)
+    for t, shape, what in ((q, (rows, cp // 2), name), (s, (rows, cp // 32), name + " scales")):
+        if t.device != device or t.dtype != torch.uint8 or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous uint8 on {device}")
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _out_matrix(out, shape, dtype, device, name: str) -> torch.Tensor:
+    """The output matrix: given (checked) or new."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _matrix(out, name)
+    if tuple(out.shape) != tuple(shape) or out.device != device:
+        raise ValueError(f"{name} must have shape {tuple(shape)} on {device}")
+    if out.shape[0] > 1 and out.stride(0) < out.shape[1]:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return out
+
+
+class _on:
+    """Makes `device` and, if one is given, `stream` current: outputs and
+    scratch then belong to the stream that the kernels run on.  `handle` is
+    the stream's handle.  The usual case, the current device and its current
+    stream, costs two comparisons."""
+    __slots__ = ("handle", "_ctx")
+
+    def __init__(self, device: torch.device, stream):
+        index = device.index
+        if stream is None and index == torch.cuda.current_device():
+            self._ctx = None
+        elif stream is None:
+            self._ctx = torch.cuda.device(index)
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+                stream = (torch.cuda.ExternalStream(handle, device=device) if handle
+                          else torch.cuda.default_stream(device))
+            if stream.device != device:
+                raise ValueError(f"stream must be on {device}")
+            self._ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        self.handle = torch.cuda.current_stream().cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+        return False
+
+
+def moe_mxfp4_quant(x: torch.Tensor, rows: bool = True, cols: bool = False, stream=None):
+    """MXFP4 quantisation of bf16/f32 x [R, C] along its rows and / or its
+    columns from one read.  -> (q_row uint8 [R, Cp/2], s_row uint8 [R, Cp/32],
+    q_col uint8 [C, Rp/2], s_col uint8 [C, Rp/32]), None where not asked for;
+    Cp, Rp: C, R rounded up to 128.  A group of 32 that holds an infinity or a
+    NaN gets scale 255 (NaN)."""
+    dt = _matrix(x, "x")
+    if not rows and not cols:
+        raise ValueError("rows or cols must be set")
+    R, C = x.shape
+    with _on(x.device, stream) as on:
+        new = lambda n, m: torch.empty(n, m, dtype=torch.uint8, device=x.device)
+        q_row, s_row = (new(R, _padded(C) // 2), new(R, _padded(C) // 32)) if rows else (None, None)
+        q_col, s_col = (new(C, _padded(R) // 2), new(C, _padded(R) // 32)) if cols else (None, None)
+        if R and C:
+            _check(_lib.moe_mxfp4_quant(x.data_ptr(), dt, R, C, _ld(x), q_row.data_ptr() if rows else None,
+                                        s_row.data_ptr() if rows else None, q_col.data_ptr() if cols else None,
+                                        s_col.data_ptr() if cols else None, on.handle), "moe_mxfp4_quant")
+    return q_row, s_row, q_col, s_col
+
+
+def moe_mxfp4_dequant(q: torch.Tensor, s: torch.Tensor, cols: int, dtype: torch.dtype = torch.bfloat16,
+                      out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values [R, cols] that MXFP4 codes and scales stand for (exact)."""
+    if not q.is_cuda:
+        raise ValueError("q must be a device tensor")
+    _codes(q, s, q.shape[0], cols, q.device, "q")
+    _float_dtype(dtype, "dtype")
+    with _on(q.device, stream) as on:
+        out = _out_matrix(out, (q.shape[0], cols), dtype, q.device, "out")
+        _check(_lib.moe_mxfp4_dequant(q.data_ptr(), s.data_ptr(), q.shape[0], cols, _FLOAT_DTYPES[out.dtype],
+                                      out.data_ptr(), _ld(out), on.handle), "moe_mxfp4_dequant")
+    return out
+
+
+def moe_mxfp4_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
+                     out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                     accumulate: bool = False, stream=None) -> torch.Tensor:
+    """deq(a) deq(b)^T, a [M, K] and b [N, K] quantised along K (the padded K
+    is taken from the codes).  accumulate adds to a given f32 `out`."""
+    if not a.is_cuda or a.dim() != 2 or b.dim() != 2:
+        raise ValueError("a and b must be device matrices of codes")
+    M, N, K = a.shape[0], b.shape[0], a.shape[1] * 2
+    if K % 128:
+        raise ValueError("a must have rows of a multiple of 64 bytes")
+    _codes(a, a_scale, M, K, a.device, "a")
+    _codes(b, b_scale, N, K, a.device, "b")
+    _float_dtype(out_dtype, "out_dtype")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    with _on(a.device, stream) as on:
+        out = _out_matrix(out, (M, N), out_dtype, a.device, "out")
+        need = _lib.moe_mxfp4_matmul_bytes(M, N, K)
+        ws = _empty_bytes(need, a.device) if need else None
+        _check(_lib.moe_mxfp4_matmul(M, N, K, a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(),
+                                     _FLOAT_DTYPES[out.dtype], out.data_ptr(), _ld(out), int(accumulate),
+                                     ws.data_ptr() if need else None, need, on.handle), "moe_mxfp4_matmul")
+    return out
+
+
+def moe_mxfp4_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                     out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Q(x) deq(w)^T: bf16/f32 x [M, K], quantised on the way, times MXFP4
+    weights w [N, K] (quantised along K)."""
+    dt = _matrix(x, "x")
+    M, K = x.shape
+    N = w.shape[0]
+    _codes(w, w_scale, N, K, x.device, "w")
+    _float_dtype(out_dtype, "out_dtype")
+    with _on(x.device, stream) as on:
+        out = _out_matrix(out, (M, N), out_dtype, x.device, "out")
+        need = _lib.moe_mxfp4_linear_bytes(M, N, K)
+        ws = _empty_bytes(need, x.device)
+        _check(_lib.moe_mxfp4_linear(M, N, K, x.data_ptr(), dt, _ld(x), w.data_ptr(), w_scale.data_ptr(),
+                                     _FLOAT_DTYPES[out.dtype], out.data_ptr(), _ld(out), ws.data_ptr(), need,
+                                     on.handle), "moe_mxfp4_linear")
+    return out
+
+
+def moe_mxfp4_linear_bwd(dy: torch.Tensor, x_col=None, w_col=None, dx_dtype: torch.dtype = torch.bfloat16,
+                         dx: torch.Tensor | None = None, dw: torch.Tensor | None = None, accumulate: bool = False,
+                         stream=None):
+    """Gradients of y = Q(x) deq(w)^T from bf16/f32 dy [M, N].  x_col, w_col:
+    (codes, scales) of x [M, K] and w [N, K] along their columns, as
+    moe_mxfp4_quant(..., cols=True) gives them.  -> (dx [M, K], or None without
+    w_col; dw f32 [N, K], or None without x_col).  accumulate adds to a given dw."""
+    dt = _matrix(dy, "dy")
+    M, N = dy.shape
+    if x_col is None and w_col is None:
+        raise ValueError("x_col or w_col must be given")
+    if accumulate and (dw is None or x_col is None):
+        raise ValueError("accumulate needs x_col and dw")
+    K = (x_col if x_col is not None else w_col)[0].shape[0]
+    dev = dy.device
+    if x_col is not None:
+        _codes(*x_col, K, M, dev, "x_col")
+    elif dw is not None:
+        raise ValueError("dw needs x_col")
+    if w_col is not None:
+        _codes(*w_col, K, N, dev, "w_col")
+    elif dx is not None:
+        raise ValueError("dx needs w_col")
+    if dw is not None and dw.dtype != torch.float32:
+        raise ValueError("dw must be f32")
+    _float_dtype(dx_dtype, "dx_dtype")
+    with _on(dev, stream) as on:
+        if w_col is not None:
+            dx = _out_matrix(dx, (M, K), dx_dtype, dev, "dx")
+        if x_col is not None:
+            dw = _out_matrix(dw, (N, K), torch.float32, dev, "dw")
+        need = _lib.moe_mxfp4_linear_bwd_bytes(M, N, K)
+        ws = _empty_bytes(need, dev)
+        ptr = lambda t: t.data_ptr() if t is not None else None
+        xq, xs = x_col if x_col is not None else (None, None)
+        wq, ws_ = w_col if w_col is not None else (None, None)
+        if K and (M or N):
+            _check(_lib.moe_mxfp4_linear_bwd(M, N, K, dy.data_ptr(), dt, _ld(dy), ptr(xq), ptr(xs), ptr(wq), ptr(ws_),
+                                             _FLOAT_DTYPES[dx.dtype] if dx is not None else MOE_DTYPE_BF16, ptr(dx),
+                                             _ld(dx) if dx is not None else 0, ptr(dw),
+                                             _ld(dw) if dw is not None else 0, int(accumulate), ws.data_ptr(), need,
+                                             on.handle), "moe_mxfp4_linear_bwd")
+    return dx, dw
+
+
+# ---- training the router --------------------------------------------------------
+
+def _router_tensors(logits, ids, token_mask, seq_offsets, named):
+    """Checks the router's tensors; -> (T, E, k, num_seqs)."""
+    if not logits.is_cuda or logits.dim() != 2:
+        raise ValueError("logits must be a device matrix")
+    T, E = logits.shape
+    S = 1
+    if seq_offsets is not None:
+        if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
+            raise ValueError("seq_offsets must hold num_seqs + 1 values")
+        S = seq_offsets.shape[0] - 1
+    if ids.dim() != 2:
+        raise ValueError("ids must be a matrix")
+    k = ids.shape[1]
+    for t, dtype, shape, name in ((logits, torch.float32, (T, E), "logits"), (ids, torch.int32, (T, k), "ids"),
+                                  (token_mask, (torch.uint8, torch.bool), (T,), "token_mask"),
+                                  (seq_offsets, torch.int32, (S + 1,), "seq_offsets"), *named(T, E, k, S)):
+        if t is None:
+            continue
+        if t.device != logits.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous on {logits.device}")
+        if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return T, E, k, S
+
+
+def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, token_mask: torch.Tensor | None = None,
+                     seq_offsets: torch.Tensor | None = None, stream=None):
+    """Balance loss, z loss and per-expert counts of routed tokens.  logits
+    f32 [T, E], ids int32 [T, k], token_mask uint8/bool [T] (0: left out),
+    seq_offsets int32 [S + 1] (default: one sequence of all tokens).
+    -> (loss f32 [2], counts int32 [S, E], seq_tokens int32 [S + 2], lse f32 [T])."""
+    T, E, k, S = _router_tensors(logits, ids, token_mask, seq_offsets, lambda *_: ())
+    dev = logits.device
+    with _on(dev, stream) as on:
+        loss = torch.empty(2, dtype=torch.float32, device=dev)
+        counts = torch.empty(S, E, dtype=torch.int32, device=dev)
+        seq_tokens = torch.empty(S + 2, dtype=torch.int32, device=dev)
+        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        need = _lib.moe_balance_bytes(T, E, S)
+        ws = _empty_bytes(need, dev)
+        _check(_lib.moe_balance_loss(logits.data_ptr(), ids.data_ptr(), T, E, k,
+                                     token_mask.data_ptr() if token_mask is not None else None,
+                                     seq_offsets.data_ptr() if seq_offsets is not None else None, S, loss.data_ptr(),
+                                     counts.data_ptr(), seq_tokens.data_ptr(), lse.data_ptr(), ws.data_ptr(), need,
+                                     on.handle), "moe_balance_loss")
+    return loss, counts, seq_tokens, lse
+
+
+def moe_router_bwd(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor | None = None,
+                   d_weights: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                   counts: torch.Tensor | None = None, seq_tokens: torch.Tensor | None = None,
+                   d_loss: torch.Tensor | None = None, token_mask: torch.Tensor | None = None,
+                   seq_offsets: torch.Tensor | None = None, d_logits: torch.Tensor | None = None, stream=None):
+    """Gradient f32 [T, E] to the router's logits: of moe_balance_loss's two
+    losses (d_loss f32 [2], with the lse, counts and seq_tokens it gave) and of
+    moe_route_topk's weights (d_weights f32 [T, k]); either may be left out."""
+    if d_weights is None and d_loss is None:
+        raise ValueError("d_weights or d_loss must be given")
+    if d_weights is not None and weights is None:
+        raise ValueError("d_weights needs weights")
+    if d_loss is not None and (lse is None or counts is None or seq_tokens is None):
+        raise ValueError("d_loss needs lse, counts and seq_tokens")
+    T, E, k, S = _router_tensors(logits, ids, token_mask, seq_offsets, lambda T, E, k, S: (
+        (weights, torch.float32, (T, k), "weights"), (d_weights, torch.float32, (T, k), "d_weights"),
+        (lse, torch.float32, (T,), "lse"), (counts, torch.int32, (S, E), "counts"),
+        (seq_tokens, torch.int32, (S + 2,), "seq_tokens"), (d_loss, torch.float32, (2,), "d_loss"),
+        (d_logits, torch.float32, (T, E), "d_logits")))
+    ptr = lambda t: t.data_ptr() if t is not None else None
+    with _on(logits.device, stream) as on:
+        if d_logits is None:
+            d_logits = torch.empty(T, E, dtype=torch.float32, device=logits.device)
+        _check(_lib.moe_router_bwd(logits.data_ptr(), ids.data_ptr(), ptr(weights), ptr(d_weights), T, E, k,
+                                   ptr(token_mask), ptr(seq_offsets), S, ptr(lse), ptr(counts), ptr(seq_tokens),
+                                   ptr(d_loss), d_logits.data_ptr(), on.handle), "moe_router_bwd")
+    return d_logits
 
 
 def moe_diag_mfma_tile(kind: int, a: torch.Tensor, b: torch.Tensor, stream=None) -> torch.Tensor:
