@@ -382,7 +382,7 @@ moe_status_t moe_forward(const moe_cfg_t* cfg, int32_t T, const void* x_bf16, in
  * u8 [rows, Cp/2] with E8M0 scales u8 [rows, Cp/32], Cp = cols rounded up to
  * 128, grouped along the row: the layout of moe_quant_act.  The codes past
  * `cols` have to be zero, as the quantisers write them.  All sizes may be
- * zero; each is at most 2^24, and a (padded) matrix at most 2^40 elements.
+ * zero; each is at most 2^24, and a (padded) matrix at most 2^38 elements.
  * Alignment: codes 16 bytes, scales 4, workspaces 16, other matrices their
  * element's size; else MOE_ERR_ALIGN.  Row strides are in elements and not
  * below the row's length.  Outputs must not overlap inputs or workspaces. */

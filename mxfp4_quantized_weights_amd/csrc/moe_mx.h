@@ -11,7 +11,7 @@
 namespace moe {
 
 constexpr int64_t kMxMaxDim = 1ll << 24;    // rows, columns, M, N, K
-constexpr int64_t kMxMaxElems = 1ll << 40;  // elements of one matrix
+constexpr int64_t kMxMaxElems = 1ll << 38;  // elements of one matrix
 constexpr int64_t kMxMaxGrid = 1ll << 20;   // workgroups of a launch (the kernels step over what is left)
 
 inline __host__ __device__ int64_t mx_padded(int64_t n) { return (n + 127) / 128 * 128; }

@@ -9,6 +9,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/moe.h"
 #include "moe_device.h"
 #include "moe_mx.h"
@@ -16,6 +18,12 @@
 namespace moe {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+// The same at any element's address: the hardware takes vector accesses that
+// are aligned to no more than their elements.
+typedef uint32_t v4u_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t v2u_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef float v4f_any __attribute__((ext_vector_type(4), aligned(2)));
 
 struct MxMatmulArgs {
   const uint8_t *a, *as, *b, *bs;
@@ -23,45 +31,16 @@ struct MxMatmulArgs {
   void* out;
   int64_t ld;
   int32_t accumulate;
-  int32_t vec;              // rows of out take 16-byte stores
   uint32_t tiles_m, tiles_n, pieces;
   int64_t piece_kb;         // K blocks of one piece of a split sum
-  float* part;              // [pieces][M][N] partial sums
+  int64_t piece_bytes;      // between the pieces' outputs
 };
 
-// Eight outputs of a row from element `at`, `left` of them inside it.  vec:
-// 16-byte accesses are aligned.
-template <bool BF16>
-__device__ __forceinline__ void mx_store8(void* out, int64_t at, int64_t left, bool vec, bool accumulate,
-                                          const float (&v)[8]) {
-  if constexpr (BF16) {
-    uint16_t* o = (uint16_t*)out + at;
-    uint32_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = f32_to_bf16(v[2 * i]) | (uint32_t)f32_to_bf16(v[2 * i + 1]) << 16;
-    if (vec && left >= 8) {
-      *(uint4*)o = make_uint4(h[0], h[1], h[2], h[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) o[i] = (uint16_t)(h[i / 2] >> (16 * (i & 1)));
-    }
-  } else {
-    float* o = (float*)out + at;
-    if (vec && left >= 8) {
-      float4 a = make_float4(0, 0, 0, 0), b = a;
-      if (accumulate) {
-        a = *(const float4*)o;
-        b = *(const float4*)(o + 4);
-      }
-      *(float4*)o = make_float4(a.x + v[0], a.y + v[1], a.z + v[2], a.w + v[3]);
-      *(float4*)(o + 4) = make_float4(b.x + v[4], b.y + v[5], b.z + v[6], b.w + v[7]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) o[i] = accumulate ? o[i] + v[i] : v[i];
-    }
-  }
+// Two fp32 values rounded to bf16 (nearest even; the hardware conversion).
+__device__ __forceinline__ uint32_t mx_bf16x2(float a, float b) {
+  typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+  const v2bf h = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, h);
 }
 
 // LDS written by some lanes of a wave is read by others of the same wave: a
@@ -107,12 +86,13 @@ __device__ __forceinline__ v16f mfma_fp4_32(const uint4& a, const uint4& b, v16f
 template <int MT, int NT>
 struct MxTile {
   static constexpr int BM = 64 * MT, BN = 64 * NT, ROWS = BM + BN;
-  static constexpr int CODES = ROWS * 128;          // a rows, then b rows
-  static constexpr int STAGE = CODES + ROWS * 8;    // scales: [half][row] dwords
-  static constexpr int LDS = 2 * STAGE;
-  static constexpr int CHUNKS = ROWS / 8 / 4;       // 1 KB loads (8 rows) per wave and stage
-  static constexpr int SCALES = ROWS / 64 * 2 / 4;  // 256-byte scale loads per wave and stage (of 64 rows, one half)
-  static_assert(ROWS % 128 == 0, "every wave issues the same number of loads");
+  static constexpr int CODES = ROWS * 128;            // one stage's codes: a rows, then b rows
+  static constexpr int GROUP = ROWS * 16;             // scales of two stages: [row][four halves' dwords]
+  static constexpr int CHUNKS = ROWS / 8 / 4;         // 1 KB loads (8 rows) per wave and stage
+  static constexpr int SCALES = (ROWS / 64 + 3) / 4;  // 1 KB scale loads (64 rows) per wave and two stages
+  static constexpr int BUFFERS = 2 * (CODES + GROUP);
+  static constexpr int LDS = BUFFERS + 64;            // scale reads past the last half reach up to 40 bytes over
+  static_assert(ROWS % 128 == 0 && BUFFERS >= 4 * 4096, "load split; room for the turned rows");
 };
 
 #pragma clang diagnostic push
@@ -128,20 +108,95 @@ __device__ __forceinline__ const uint8_t* mx_uniform(const uint8_t* p) {
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32));
   return (const uint8_t*)((uint64_t)hi << 32 | lo);
 }
-// 16 (4) bytes per lane from base + off to LDS at lds + 16 (4) * lane.
-__device__ __forceinline__ void mx_dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(mx_uniform(base)), "s"(__builtin_amdgcn_readfirstlane(lds))
-               : "memory", "m0");
-}
-__device__ __forceinline__ void mx_dma4(const uint8_t* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(mx_uniform(base)), "s"(__builtin_amdgcn_readfirstlane(lds))
-               : "memory", "m0");
+// 16 bytes per lane (none where `lanes` is 0, else -1) from base + off to LDS at lds + 16 * lane.  Every
+// lane of the wave is active here, before and after.
+__device__ __forceinline__ void mx_dma16(const uint8_t* base, uint32_t off, uint32_t lds, int lanes) {
+  asm volatile(
+      "s_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1\n\ts_mov_b64 exec, -1" ::"v"(off),
+      "s"(mx_uniform(base)), "s"(__builtin_amdgcn_readfirstlane(lds)), "s"(__builtin_amdgcn_readfirstlane(lanes))
+      : "memory", "m0");
 }
 #pragma clang diagnostic pop
 
 // Everything this wave has loaded and read has arrived, then all waves meet.
 __device__ __forceinline__ void mx_wait_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// A wave's (32 MT) x (32 NT) results, from row m0 and column n0 on, to out
+// [M, N] (row stride ld).  Blocks of 32 rows x 128 bytes are turned in 4 KB of
+// the wave's own LDS from the lanes' runs of four columns into whole rows:
+// 16-byte unit c of row r lies in place c ^ (r % 8), so that neither side's
+// accesses collide.
+template <int MT, int NT, bool BF16>
+__device__ __forceinline__ void mx_write_tile(const v16f (&acc)[MT][NT], uint8_t* turn, void* out, int64_t ld, bool accumulate,
+                                              int64_t m0, int64_t n0, int64_t M, int64_t N) {
+  constexpr int E = BF16 ? 2 : 4;                  // bytes of an element
+  constexpr int W = NT * 32 * E < 128 ? NT * 32 * E : 128;  // bytes of a block's row
+  constexpr int JN = W / E / 32;                   // 32-column tiles of a block
+  constexpr int UNITS = W / 16, ROWS = 64 / UNITS, LOADS = 32 / ROWS;  // a load: ROWS rows, 1 KB
+  static_assert(ROWS % UNITS == 0, "the rotation is the same in every load");
+  const uint32_t lane = threadIdx.x & 63;
+  const int64_t stride = ld;
+  const uint32_t r = lane & 31, g = lane >> 5;
+  const uint32_t row0 = lane / UNITS, c0 = lane % UNITS;
+  const int rows = (int)min((int64_t)32 * MT, M - m0), cols = (int)min((int64_t)32 * NT, N - n0);
+  if (rows <= 0 || cols <= 0) return;
+  uint8_t* const base = (uint8_t*)out + (m0 * ld + n0) * E;
+  const bool whole = cols == 32 * NT && rows == 32 * MT;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+#pragma unroll
+    for (int j0 = 0; j0 < NT; j0 += JN) {
+#pragma unroll
+      for (int j = j0; j < j0 + JN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const v16f& a = acc[i][j];
+          if constexpr (BF16)
+            *(uint2*)(turn + (r * UNITS + (((j - j0) * 4 + q) ^ (r & (UNITS - 1)))) * 16 + 8 * g) =
+                make_uint2(mx_bf16x2(a[4 * q], a[4 * q + 1]), mx_bf16x2(a[4 * q + 2], a[4 * q + 3]));
+          else
+            *(float4*)(turn + (r * UNITS + (((j - j0) * 8 + 2 * q + g) ^ (r & (UNITS - 1)))) * 16) =
+                make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+        }
+      mx_wave_lds_sync();
+      const uint8_t* from = turn + (row0 * UNITS + (c0 ^ (row0 & (UNITS - 1)))) * 16;
+      uint8_t* to = base + (int64_t)(i * 32 + row0) * stride * E + j0 * 32 * E + c0 * 16;
+      if (whole && (BF16 || !accumulate)) {
+        v4u x[LOADS];
+#pragma unroll
+        for (int t = 0; t < LOADS; ++t) x[t] = *(const v4u*)(from + t * 1024);
+#pragma unroll
+        for (int t = 0; t < LOADS; ++t) __builtin_nontemporal_store(x[t], (v4u_any*)(to + (int64_t)t * ROWS * E * stride));
+      } else {
+        const int left = cols - j0 * 32 - (int)c0 * (16 / E);  // columns from the lane's first on
+#pragma unroll
+        for (int t = 0; t < LOADS; ++t) {
+          if (i * 32 + (int)row0 + t * ROWS >= rows || left <= 0) continue;
+          uint8_t* o = to + (int64_t)t * ROWS * E * stride;
+          const uint8_t* x = from + t * 1024;
+          if (left >= 16 / E) {
+            v4f v = *(const v4f*)x;
+            if (!BF16 && accumulate) {
+              v += *(const v4f_any*)o;
+            }
+            *(v4f_any*)o = v;
+          } else {
+#pragma unroll 1
+            for (int e = 0; e < left; ++e) {
+              if constexpr (BF16)
+                ((uint16_t*)o)[e] = ((const uint16_t*)x)[e];
+              else
+                ((float*)o)[e] = (accumulate ? ((float*)o)[e] : 0.0f) + ((const float*)x)[e];
+            }
+          }
+        }
+      }
+      mx_wave_lds_sync();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
 }
 
 template <int MT, int NT, bool BF16>
@@ -152,34 +207,32 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void mx_tile_kernel(MxMa
   const int r = lane & 31, g = lane >> 5;
   const int wm = wave >> 1, wn = wave & 1;
 
-  // the workgroup's tile and its share of K
+  // The workgroup's tile and its piece of K.  Workgroups go round the 8 XCDs:
+  // each XCD gets a contiguous part of the list of (piece, tile) items, in
+  // which runs of GM tile rows share their b columns.
   int64_t m0, n0;
   int piece;
   {
-    // workgroups go round the 8 XCDs: each XCD gets a contiguous part of the
-    // list, in which runs of GM tile rows share their b columns
-    const uint32_t total = p.tiles_m * p.tiles_n * p.pieces, bid = blockIdx.x;
-    const uint32_t per = total / 8, rest = total % 8, x = bid % 8;
-    uint32_t i = x * per + min(x, rest) + bid / 8;
-    const uint32_t tiles = p.tiles_m * p.tiles_n;
+    const uint32_t tiles = p.tiles_m * p.tiles_n, total = tiles * p.pieces;
+    const uint32_t xcd = blockIdx.x % 8, share = total / 8, rest = total % 8;
+    uint32_t i = xcd * share + min(xcd, rest) + blockIdx.x / 8;
     piece = (int)(i / tiles);
     i -= piece * tiles;
-    constexpr uint32_t GM = 8;
+        constexpr uint32_t GM = 4;
     const uint32_t band = i / (GM * p.tiles_n), first = band * GM;
     const uint32_t height = min(GM, p.tiles_m - first), j = i - band * GM * p.tiles_n;
     m0 = (int64_t)(first + j % height) * T::BM;
     n0 = (int64_t)(j / height) * T::BN;
   }
   const int64_t kb0 = (int64_t)piece * p.piece_kb;
-  const int kb = (int)min(p.piece_kb, p.kb - kb0);  // 128-wide halves of this workgroup
+  const int kb = __builtin_amdgcn_readfirstlane((int)min(p.piece_kb, p.kb - kb0));  // 128-wide halves of this workgroup
   const int stages = (kb + 1) / 2;
-
+  const uint8_t* base_a = mx_uniform(p.a + (m0 * p.kb + kb0) * 64);
+  const uint8_t* base_b = mx_uniform(p.b + (n0 * p.kb + kb0) * 64);
+  const uint8_t* base_as = mx_uniform(p.as + (m0 * p.kb + kb0) * 4);
+  const uint8_t* base_bs = mx_uniform(p.bs + (n0 * p.kb + kb0) * 4);
   // Source offsets of this wave's loads, from the tile's first row.  Rows past
   // the matrix are read as its last row; their results are not stored.
-  const uint8_t* base_a = p.a + (m0 * p.kb + kb0) * 64;
-  const uint8_t* base_b = p.b + (n0 * p.kb + kb0) * 64;
-  const uint8_t* base_as = p.as + (m0 * p.kb + kb0) * 4;
-  const uint8_t* base_bs = p.bs + (n0 * p.kb + kb0) * 4;
   const int rows_a = (int)min((int64_t)T::BM, p.M - m0), rows_b = (int)min((int64_t)T::BN, p.N - n0);
   uint32_t off[T::CHUNKS], soff[T::SCALES];
 #pragma unroll
@@ -190,205 +243,329 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void mx_tile_kernel(MxMa
   }
 #pragma unroll
   for (int q = 0; q < T::SCALES; ++q) {
-    const int c = wave * T::SCALES + q, row = c / 2 * 64 + lane;
+    const int row = min(wave * T::SCALES + q, T::ROWS / 64 - 1) * 64 + lane;
     const uint32_t in = row < T::BM ? min(row, rows_a - 1) : min(row - T::BM, rows_b - 1);
-    soff[q] = in * (uint32_t)p.kb * 4u + (c & 1) * 4;
+    soff[q] = in * (uint32_t)p.kb * 4u;
   }
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
 
-  // Loads of stage st.  In a last stage of one half the other half's bytes
-  // lie past the row: the first half is loaded twice and not used again.
-  auto issue = [&](int st) {
-    const uint32_t to = lds0 + (st & 1) * T::STAGE;
+  // Load x of stage st.  In a last stage of one half (`single`) the other
+  // half's bytes lie past the row: the first half is loaded twice, and the
+  // second not used.  A lane's piece lies in the second half where bit 2 of
+  // its slot differs from bit 2 of the rotation, which is bit 0 of the chunk.
+  auto issue1 = [&](int st, int x, uint32_t back0, uint32_t back1, int lanes, bool even) __attribute__((always_inline)) {
+    if (x < T::CHUNKS) {
+      const int c = wave * T::CHUNKS + x;
+      mx_dma16((c * 8 < T::BM ? base_a : base_b) + (int64_t)st * 128, off[x] - (c & 1 ? back1 : back0),
+               lds0 + (st & 1) * T::CODES + c * 1024, lanes);
+    } else if (even) {
+      // scales come for four halves at a time, the last four of the row where
+      // fewer are left
+      const int q = x - T::CHUNKS, c = min(wave * T::SCALES + q, T::ROWS / 64 - 1);
+      mx_dma16((c * 64 < T::BM ? base_as : base_bs) + (int64_t)min(2 * st, kb - 4) * 4, soff[q],
+               lds0 + 2 * T::CODES + ((st >> 1) & 1) * T::GROUP + c * 1024, lanes);
+    }
+  };
+  auto issue = [&](int st) __attribute__((always_inline)) {
     const bool single = 2 * st + 1 >= kb;
+    const uint32_t back0 = single ? (lane & 4) << 4 : 0, back1 = single ? (~lane & 4) << 4 : 0;
 #pragma unroll
-    for (int q = 0; q < T::CHUNKS; ++q) {
-      const int c = wave * T::CHUNKS + q;
-      const uint8_t* base = (c * 8 < T::BM ? base_a : base_b) + (int64_t)st * 128;
-      // a lane's piece lies in the second half where bit 2 of its slot differs
-      // from bit 2 of the rotation, which is bit 0 of c
-      mx_dma16(base, single ? off[q] - (((lane ^ (c << 2)) & 4) << 4) : off[q], to + c * 1024);
-    }
-#pragma unroll
-    for (int q = 0; q < T::SCALES; ++q) {
-      const int c = wave * T::SCALES + q;
-      const uint8_t* base = (c / 2 * 64 < T::BM ? base_as : base_bs) + (int64_t)st * 8;
-      mx_dma4(base, single && (c & 1) ? soff[q] - 4 : soff[q], to + T::CODES + ((c & 1) * T::ROWS + c / 2 * 64) * 4);
-    }
+    for (int x = 0; x < T::CHUNKS + T::SCALES; ++x) issue1(st, x, back0, back1, -1, !(st & 1));
   };
 
   v16f acc[MT][NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = v16f{};
-
-  // Fragments of a 128-wide half u (both 64-wide steps): all b tiles of the
-  // half, the a tiles two ahead.
+  // Fragments of a 128-wide half (two 64-wide steps).
   struct Frag {
     uint4 v[2];
     uint32_t s;
   };
-  Frag fb[NT], nb[NT], fa[MT + 1];
-  const int swz = (r >> 1) & 7;
-  auto read = [&](Frag& f, int row, int u) {
-    const int h = u & 1;
-    const uint8_t* buf = lds + ((u >> 1) & 1) * T::STAGE;
-    f.v[0] = *(const uint4*)(buf + row * 128 + ((4 * h + 2 * g) ^ swz) * 16);
-    f.v[1] = *(const uint4*)(buf + row * 128 + ((4 * h + 2 * g + 1) ^ swz) * 16);
-    f.s = *(const uint32_t*)(buf + T::CODES + (h * T::ROWS + row) * 4) >> (16 * g);
+  Frag fb[2][NT], fa[MT + 1];
+  // Addresses of the lane's first a and b row: codes by (half of a stage,
+  // step), stage buffer 0; scales of the current and the next group of four
+  // halves.
+  const int row_a = wm * MT * 32 + r, row_b = T::BM + wn * NT * 32 + r, swz = (r >> 1) & 7;
+  uint32_t ca[2][2][2], cb_[2][2][2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int o = (i >> 2) * T::CODES + ((4 * ((i >> 1) & 1) + 2 * g + (i & 1)) ^ swz) * 16;
+    ca[i >> 2][(i >> 1) & 1][i & 1] = row_a * 128 + o;
+    cb_[i >> 2][(i >> 1) & 1][i & 1] = row_b * 128 + o;
+  }
+  auto group_at = [&](int q) __attribute__((always_inline)) -> uint32_t {  // offset of group q's first half in LDS
+    return 2 * T::CODES + (q & 1) * T::GROUP + (4 * q - min(4 * q, kb - 4)) * 4;
   };
-  const int row_a = wm * MT * 32 + r, row_b = T::BM + wn * NT * 32 + r;
-  // One half.  The next half's b tiles and first a tile are read during the
-  // last tile rows (past the last half: whatever LDS holds, not used).  Where
-  // that half lies in the next stage (publish), the stage has to have arrived
-  // first, for all waves, and this stage's buffer is free from then on.
-  constexpr int kLead = MT >= 2 ? 2 : 1;  // tile rows that cover the next half's reads
-  auto half = [&](int u, bool publish) __attribute__((always_inline)) {
+  // part 0, 1: the steps' codes; 2: the scales.  k: half within its group of four.
+  auto read_a = [&](Frag& f, int i, int k, uint32_t sc, int part) __attribute__((always_inline)) {
+    if (part < 2)
+      f.v[part] = *(const uint4*)(lds + ca[k >> 1][k & 1][part] + i * 4096);
+    else
+      f.s = *(const uint32_t*)(lds + sc + row_a * 16 + i * 512 + k * 4);
+  };
+  auto read_b = [&](Frag& f, int j, int k, uint32_t sc, int part) __attribute__((always_inline)) {
+    if (part < 2)
+      f.v[part] = *(const uint4*)(lds + cb_[k >> 1][k & 1][part] + j * 4096);
+    else
+      f.s = *(const uint32_t*)(lds + sc + row_b * 16 + j * 512 + k * 4);
+  };
+  constexpr int kMfma = 2 * MT * NT;
+  constexpr int kPub = MT >= 2 ? (MT - 2) * NT * 2 : 0;  // the instruction before which stages change hands
+  constexpr int kSlots = kMfma - kPub;
+  constexpr int kReadSlots = kSlots * 3 / 4;  // the reads, a little ahead of their use; the loads over all of them
+  // Half k of group q.  Halves past the end are multiplied with scales of
+  // 2^-127 on both sides, whose products vanish in fp32.
+  auto half = [&](int q, int k, uint32_t sc, uint32_t sc_next, Frag (&cb)[NT], Frag (&nb)[NT]) __attribute__((always_inline)) {
+    const int u = 4 * q + k;
+    const uint32_t width = u < kb ? 16 : 0;
+    uint32_t sb[NT], sa = 0;
+    const int st = (u >> 1) + 2;
+    const bool more = st < stages, single = 2 * st + 1 >= kb;
+    uint32_t back0 = 0, back1 = 0;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if (i < MT - 1 && i <= MT - kLead) read(fa[i + 1], row_a + (i + 1) * 32, u);
-      if (i == MT - kLead) {
-        // every a tile of this half is in registers or on the way
-        if (publish) {
-          mx_wait_barrier();
-          const int st = (u >> 1) + 2;
-          if (st < stages) issue(st);
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j) read(nb[j], row_b + j * 32, u + 1);
-        read(fa[MT], row_a, u + 1);
+    for (int n = 0; n < kMfma; ++n) {
+      const int i = n / (2 * NT), t = n % (2 * NT), j = t % NT;
+      if (n == kPub && (k & 1)) {
+        mx_wait_barrier();
+        back0 = single ? (lane & 4) << 4 : 0;
+        back1 = single ? (~lane & 4) << 4 : 0;
       }
+      __builtin_amdgcn_sched_barrier(0);
+      if (t == 0) sa = __builtin_amdgcn_ubfe(fa[i].s, 16 * g, width);
+      if (i == 0 && t < NT) sb[j] = __builtin_amdgcn_ubfe(cb[j].s, 16 * g, width);
+      if (t < NT)
+        acc[i][j] = mfma_fp4_32<0>(cb[j].v[0], fa[i].v[0], acc[i][j], sb[j], sa);
+      else
+        acc[i][j] = mfma_fp4_32<1>(cb[j].v[1], fa[i].v[1], acc[i][j], sb[j], sa);
+      __builtin_amdgcn_sched_barrier(0);
+      // a tiles 1 .. MT-1: all before kPub
+      constexpr int kA = 3 * (MT - 1), kSlotsA = kPub > 0 ? kPub - 1 : 1;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = mfma_fp4_32<0>(fb[j].v[0], fa[i].v[0], acc[i][j], fb[j].s, fa[i].s);
+      for (int x = 0; x < kA; ++x)
+        if (x * kSlotsA / (kA > 0 ? kA : 1) == n) read_a(fa[1 + x / 3], 1 + x / 3, k, sc, 2 - x % 3);
+      // the next half, from kPub on
+      constexpr int kN = 3 * (NT + 1);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = mfma_fp4_32<1>(fb[j].v[1], fa[i].v[1], acc[i][j], fb[j].s, fa[i].s);
+      for (int x = 0; x < kN; ++x)
+        if (kPub + x * kReadSlots / kN == n) {
+          if (x < 3)
+            read_a(fa[MT], 0, (k + 1) & 3, k == 3 ? sc_next : sc, 2 - x % 3);
+          else
+            read_b(nb[x / 3 - 1], x / 3 - 1, (k + 1) & 3, k == 3 ? sc_next : sc, 2 - x % 3);
+        }
+      if ((k & 1) && n >= kPub) {
+        constexpr int kL = T::CHUNKS + T::SCALES;
+#pragma unroll
+        for (int x = 0; x < kL; ++x)
+          if (kPub + x * kSlots / kL == n) issue1(st, x, back0, back1, more ? -1 : 0, k == 1);
+      }
     }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) fb[j] = nb[j];
+    __builtin_amdgcn_sched_barrier(0);
     fa[0] = fa[MT];
   };
 
-  if (stages > 0) {
-    issue(0);
-    mx_wait_barrier();
-    if (stages > 1) issue(1);
+  if (kb > 0) issue(0);
+  if (stages > 1) issue(1);
 #pragma unroll
-    for (int j = 0; j < NT; ++j) read(fb[j], row_b + j * 32, 0);
-    read(fa[0], row_a, 0);
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = v16f{};
+  if (kb > 0) {
+    // stage 0 has arrived; of stage 1's loads any may still be under way
+    if (stages > 1)
+      asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(T::CHUNKS) : "memory");
+    else
+      mx_wait_barrier();
+    uint32_t sc = group_at(0);
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) read_b(fb[0][j], j, 0, sc, x);
+      read_a(fa[0], 0, 0, sc, x);
+    }
 #pragma unroll 1
-    for (int u = 0; u < kb; ++u) half(u, u & 1);
+    for (int q = 0; 4 * q < kb; ++q) {
+      const uint32_t sc_next = group_at(q + 1);
+      half(q, 0, sc, sc_next, fb[0], fb[1]);
+      half(q, 1, sc, sc_next, fb[1], fb[0]);
+      half(q, 2, sc, sc_next, fb[0], fb[1]);
+      half(q, 3, sc, sc_next, fb[1], fb[0]);
+      sc = sc_next;
+    }
   }
-  // every wave is done with the stage buffers, which the tile now goes through
-  // on its way out; the matrix core's last results are written before they
-  // are read
+  // every wave is done with the stage buffers, which the tile goes through on
+  // its way out; the matrix core's last results are written before they are
+  // read
   mx_wait_barrier();
   asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
+  mx_write_tile<MT, NT, BF16>(acc, lds + wave * 4096, (uint8_t*)p.out + piece * p.piece_bytes, p.ld, p.accumulate,
+                              m0 + wm * MT * 32, n0 + wn * NT * 32, p.M, p.N);
+}
 
-  // A wave turns 32 rows at a time from the lanes' runs of four columns into
-  // whole rows: 16-byte unit c of row r lies in place c ^ (r % units), so that
-  // neither side's accesses collide.
-  constexpr int UNITS = 8 * NT;  // of four fp32 values, per row of a wave's tile
-  float4* turn = (float4*)(lds + wave * 32 * UNITS * 16);
-  static_assert(4 * 32 * UNITS * 16 <= T::LDS, "the tile rows fit the stage buffers");
-  const int64_t n_wave = n0 + wn * NT * 32;
-  float* part = p.part + (int64_t)piece * p.M * p.N;
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        turn[r * UNITS + ((j * 8 + 2 * q + g) ^ (r & (UNITS - 1)))] =
-            make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
-    mx_wave_lds_sync();
-    const int64_t m_wave = m0 + (wm * MT + i) * 32;
-#pragma unroll 2
-    for (int t = lane; t < 32 * UNITS / 2; t += 64) {
-      const int row = t / (UNITS / 2), c = t % (UNITS / 2) * 2;
-      const float4 x = turn[row * UNITS + (c ^ (row & (UNITS - 1)))], y = turn[row * UNITS + ((c + 1) ^ (row & (UNITS - 1)))];
-      const int64_t m = m_wave + row, n = n_wave + c * 4;
-      if (m < p.M) {
-        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        if (p.pieces > 1)
-          mx_store8<false>(part, m * p.N + n, p.N - n, p.N % 4 == 0, false, v);
-        else
-          mx_store8<BF16>(p.out, m * p.ld + n, p.N - n, p.vec, p.accumulate, v);
-      }
+// Sums of fewer than four 128-wide blocks, too short for the stages above: one
+// wave per 32 x 32 tile, operands straight from memory.
+template <bool BF16>
+__global__ __launch_bounds__(256) void mx_short_kernel(MxMatmulArgs p, int64_t tiles_n, int64_t tiles) {
+  const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
+  for (int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); tile < tiles; tile += (int64_t)gridDim.x * 4) {
+    const int64_t m0 = tile / tiles_n * 32, n0 = tile % tiles_n * 32;
+    const int64_t m = min(m0 + r, p.M - 1), n = min(n0 + r, p.N - 1);  // rows past the end are read again
+    const uint8_t* pa = p.a + m * p.kb * 64 + 32 * g;
+    const uint8_t* pb = p.b + n * p.kb * 64 + 32 * g;
+    const uint8_t* psa = p.as + m * p.kb * 4;
+    const uint8_t* psb = p.bs + n * p.kb * 4;
+    v16f c = {};
+    for (int64_t k = 0; k < p.kb; ++k) {
+      const uint32_t sa = *(const uint32_t*)(psa + k * 4) >> (16 * g), sb = *(const uint32_t*)(psb + k * 4) >> (16 * g);
+      const uint4 a0 = *(const uint4*)(pa + k * 64), a1 = *(const uint4*)(pa + k * 64 + 16);
+      const uint4 b0 = *(const uint4*)(pb + k * 64), b1 = *(const uint4*)(pb + k * 64 + 16);
+      c = mfma_fp4_32<0>(b0, a0, c, sb, sa);
+      c = mfma_fp4_32<1>(b1, a1, c, sb, sa);
     }
-    mx_wave_lds_sync();
+    if (m0 + r >= p.M) continue;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int64_t col = n0 + 8 * (i / 4) + 4 * g + i % 4;
+      if (col >= p.N) continue;
+      const int64_t at = (m0 + r) * p.ld + col;
+      if constexpr (BF16)
+        ((uint16_t*)p.out)[at] = f32_to_bf16(c[i]);
+      else
+        ((float*)p.out)[at] = p.accumulate ? ((float*)p.out)[at] + c[i] : c[i];
+    }
   }
 }
 
 // out (+)= the pieces' sums, added in piece order.
 template <bool BF16>
-__global__ __launch_bounds__(256) void mx_join_kernel(MxMatmulArgs p) {
-  const int64_t groups = (p.N + 7) / 8, total = p.M * groups;
+__global__ __launch_bounds__(256) void mx_join_kernel(const float* __restrict__ part, int pieces, int64_t M, int64_t N,
+                                                      void* out, int64_t ld, int accumulate) {
+  const int64_t groups = (N + 3) / 4, total = M * groups;
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
-    const int64_t m = u / groups, n = (u - m * groups) * 8;
-    float v[8] = {};
-    const float* src = p.part + m * p.N + n;
-    for (int k = 0; k < (int)p.pieces; ++k, src += p.M * p.N) {
-      if (p.N % 8 == 0) {
-        const float4 a = *(const float4*)src, b = *(const float4*)(src + 4);
-        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+    const int64_t m = u / groups, n = (u - m * groups) * 4;
+    const int left = (int)min(N - n, (int64_t)4);
+    const float* src = part + m * N + n;
+    v4f v = {};
+    if (left == 4) {
+#pragma unroll 8
+      for (int k = 0; k < pieces; ++k) v += *(const v4f_any*)(src + (int64_t)k * M * N);
+    } else {
+      for (int k = 0; k < pieces; ++k)
+        for (int i = 0; i < left; ++i) v[i] += src[(int64_t)k * M * N + i];
+    }
+    if constexpr (BF16) {
+      uint16_t* o = (uint16_t*)out + m * ld + n;
+      const uint32_t h0 = mx_bf16x2(v[0], v[1]), h1 = mx_bf16x2(v[2], v[3]);
+      if (left == 4) {
+        *(v2u_any*)o = v2u_any{h0, h1};
       } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (n + i < p.N) v[i] += src[i];
+        o[0] = (uint16_t)h0;
+        if (left > 1) o[1] = (uint16_t)(h0 >> 16);
+        if (left > 2) o[2] = (uint16_t)h1;
+      }
+    } else {
+      float* o = (float*)out + m * ld + n;
+      if (left == 4) {
+        if (accumulate) v += *(const v4f_any*)o;
+        *(v4f_any*)o = v;
+      } else {
+        for (int i = 0; i < left; ++i) o[i] = accumulate ? o[i] + v[i] : v[i];
       }
     }
-    mx_store8<BF16>(p.out, m * p.ld + n, p.N - n, p.vec, p.accumulate, v);
   }
 }
 
-// The tile and the split of K for a product.
+// The tile (64 t x 64 t, t = 4, 2 or 1) and the split of K for a product.
+//
+// Time per 128-wide half, in us, with c tiles per compute unit, from sweeps of
+// 22 products on one MI355X (M 16..16384, N 300..8192, K 1000..16384): a
+// 256-tile takes 0.95 for every full or partial round of c = 1; 128-tiles
+// max(0.44, 0.36 c); 64-tiles max(0.3, 0.15 c).  The least of the three picks
+// the tile that was fastest in all of them (4096 x 4096 x 1024: 16.3 / 17.7 /
+// 25.2 us; 2048 x 4096 x 4001: 32.7 / 26.6 / 44.4; 1024 x 2048 x 4096: - /
+// 18.2 / 15.5).
+//
+// A long sum over few tiles is split into pieces, up to one workgroup per
+// compute unit (128 x 2048 x 4096, 64 tiles: 11.3 us whole, 9.8 in 4 pieces;
+// 16 x 2048 x 4096, 32 tiles: 10.9 and 7.3 in 8); at 128 tiles the join costs
+// what the split gains (256 x 2048 x 4096: 11.6 and 11.9), as it does for sums
+// of fewer than 16 halves.
 struct MxPlan {
-  int mt, nt, pieces;
+  int t, pieces;
   int64_t piece_kb;
 };
 static MxPlan mx_plan(int64_t M, int64_t N, int64_t kb) {
-  static const int kTiles[][2] = {{4, 4}, {2, 4}, {2, 2}, {1, 1}};
-  MxPlan best{1, 1, 1, kb};
-  for (const auto& t : kTiles) {
-    const int64_t tiles = ((M + 64 * t[0] - 1) / (64 * t[0])) * ((N + 64 * t[1] - 1) / (64 * t[1]));
-    best = {t[0], t[1], 1, kb};
-    if (tiles >= 192) break;
+  constexpr double kCus = 256;
+  MxPlan best{1, 1, kb};
+  double best_us = 0;
+  int64_t best_tiles = 0;
+  for (int t : {4, 2, 1}) {
+    const int64_t tiles = ((M + 64 * t - 1) / (64 * t)) * ((N + 64 * t - 1) / (64 * t));
+    const double c = (double)tiles / kCus;
+    const double us = t == 4 ? 0.95 * (double)((tiles + 255) / 256) : t == 2 ? (c * 0.36 > 0.44 ? c * 0.36 : 0.44)
+                                                                            : (c * 0.15 > 0.3 ? c * 0.15 : 0.3);
+    if (best_us == 0 || us < best_us) {
+      best.t = t;
+      best_us = us;
+      best_tiles = tiles;
+    }
+  }
+  if (best_tiles <= 64 && kb >= 16) {
+    int pieces = 1;
+    while (pieces < 16 && best_tiles * pieces * 2 <= 256 && kb / (pieces * 2) >= 4) pieces *= 2;
+    best.piece_kb = ((kb + pieces - 1) / pieces + 1) / 2 * 2;  // whole stages
+    best.pieces = (int)((kb + best.piece_kb - 1) / best.piece_kb);
   }
   return best;
 }
 
 template <int MT, int NT>
 static hipError_t launch_mx_tile(const MxMatmulArgs& p, bool bf16, hipStream_t s) {
+  const uint32_t items = p.tiles_m * p.tiles_n * p.pieces;
+  const dim3 grid(items);
   const auto run = [&](auto kernel) {
     const hipError_t e =
         hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, MxTile<MT, NT>::LDS);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3(p.tiles_m * p.tiles_n * p.pieces), dim3(256), (MxTile<MT, NT>::LDS), s, p);
+    hipLaunchKernelGGL(kernel, grid, dim3(256), (MxTile<MT, NT>::LDS), s, p);
     return hipGetLastError();
   };
   return bf16 ? run(mx_tile_kernel<MT, NT, true>) : run(mx_tile_kernel<MT, NT, false>);
 }
 
-static hipError_t launch_mx_matmul(MxMatmulArgs p, bool bf16, hipStream_t s) {
-  const MxPlan plan = mx_plan(p.M, p.N, p.kb);
-  p.pieces = plan.pieces;
-  p.piece_kb = plan.piece_kb;
-  p.tiles_m = (uint32_t)((p.M + 64 * plan.mt - 1) / (64 * plan.mt));
-  p.tiles_n = (uint32_t)((p.N + 64 * plan.nt - 1) / (64 * plan.nt));
-  p.vec = mx_vec_ok(p.out, p.ld, bf16 ? 2 : 4);
-  hipError_t e = plan.nt == 4 ? (plan.mt == 4 ? launch_mx_tile<4, 4>(p, bf16, s) : launch_mx_tile<2, 4>(p, bf16, s))
-                 : plan.nt == 2 ? launch_mx_tile<2, 2>(p, bf16, s)
-                                : launch_mx_tile<1, 1>(p, bf16, s);
-  if (e != hipSuccess || plan.pieces == 1) return e;
-  const int64_t blocks = (p.M * ((p.N + 7) / 8) + 255) / 256;
+static hipError_t launch_mx_matmul(const MxMatmulArgs& p, const MxPlan& plan, bool bf16, float* part, hipStream_t s) {
+  if (p.kb < 4) {
+    const int64_t tn = (p.N + 31) / 32, tiles = (p.M + 31) / 32 * tn, blocks = (tiles + 3) / 4;
+    const dim3 grid((unsigned)(blocks < kMxMaxGrid ? blocks : kMxMaxGrid));
+    if (bf16)
+      hipLaunchKernelGGL((mx_short_kernel<true>), grid, dim3(256), 0, s, p, tn, tiles);
+    else
+      hipLaunchKernelGGL((mx_short_kernel<false>), grid, dim3(256), 0, s, p, tn, tiles);
+    return hipGetLastError();
+  }
+  MxMatmulArgs t = p;
+  const bool split = plan.pieces > 1;
+  t.pieces = plan.pieces;
+  t.piece_kb = plan.piece_kb;
+  t.tiles_m = (uint32_t)((p.M + 64 * plan.t - 1) / (64 * plan.t));
+  t.tiles_n = (uint32_t)((p.N + 64 * plan.t - 1) / (64 * plan.t));
+  if (split) {
+    t.out = part;
+    t.ld = p.N;
+    t.accumulate = 0;
+    t.piece_bytes = p.M * p.N * 4;
+  }
+  const bool tb = bf16 && !split;
+  const hipError_t e = plan.t == 4   ? launch_mx_tile<4, 4>(t, tb, s)
+                       : plan.t == 2 ? launch_mx_tile<2, 2>(t, tb, s)
+                                     : launch_mx_tile<1, 1>(t, tb, s);
+  if (e != hipSuccess || !split) return e;
+  const int64_t blocks = (p.M * ((p.N + 3) / 4) + 255) / 256;
   const dim3 grid((unsigned)(blocks < kMxMaxGrid ? blocks : kMxMaxGrid));
   if (bf16)
-    hipLaunchKernelGGL(mx_join_kernel<true>, grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL(mx_join_kernel<true>, grid, dim3(256), 0, s, part, plan.pieces, p.M, p.N, p.out, p.ld, 0);
   else
-    hipLaunchKernelGGL(mx_join_kernel<false>, grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL(mx_join_kernel<false>, grid, dim3(256), 0, s, part, plan.pieces, p.M, p.N, p.out, p.ld,
+                       p.accumulate);
   return hipGetLastError();
 }
 
@@ -409,10 +586,15 @@ bool product_ok(int64_t M, int64_t N, int64_t K) {
   return moe::mx_matrix_ok(M, K) && moe::mx_matrix_ok(N, K) && moe::mx_matrix_ok(M, N);
 }
 
-size_t matmul_bytes(int64_t, int64_t, int64_t) { return 0; }
+// Scratch of a product: the partial sums of a split one.
+size_t matmul_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M == 0 || N == 0) return 0;
+  const moe::MxPlan plan = moe::mx_plan(M, N, mx_padded(K) / 128);
+  return plan.pieces > 1 ? up256(plan.pieces * M * N * 4) : 0;
+}
 
 moe_status_t run_matmul(int64_t M, int64_t N, int64_t K, const void* a, const void* as, const void* b, const void* bs,
-                        int32_t out_dtype, void* out, int64_t ld_out, int32_t accumulate, hipStream_t s) {
+                        int32_t out_dtype, void* out, int64_t ld_out, int32_t accumulate, void* part, hipStream_t s) {
   moe::MxMatmulArgs p{};
   p.a = (const uint8_t*)a;
   p.as = (const uint8_t*)as;
@@ -424,7 +606,7 @@ moe_status_t run_matmul(int64_t M, int64_t N, int64_t K, const void* a, const vo
   p.out = out;
   p.ld = ld_out;
   p.accumulate = accumulate;
-  return moe::mx_status(moe::launch_mx_matmul(p, out_dtype == MOE_DTYPE_BF16, s));
+  return moe::mx_status(moe::launch_mx_matmul(p, moe::mx_plan(M, N, p.kb), out_dtype == MOE_DTYPE_BF16, (float*)part, s));
 }
 
 }  // namespace
@@ -449,7 +631,7 @@ moe_status_t moe_mxfp4_matmul(int32_t M, int32_t N, int32_t K, const void* a, co
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
   if (need && !ws) return MOE_ERR_NULL;
   if (need && !mx_aligned(ws, 16)) return MOE_ERR_ALIGN;
-  return run_matmul(M, N, K, a, a_scale, b, b_scale, out_dtype, out, ld_out, accumulate, (hipStream_t)stream);
+  return run_matmul(M, N, K, a, a_scale, b, b_scale, out_dtype, out, ld_out, accumulate, ws, (hipStream_t)stream);
 }
 
 size_t moe_mxfp4_linear_bytes(int32_t M, int32_t N, int32_t K) {
@@ -478,7 +660,7 @@ moe_status_t moe_mxfp4_linear(int32_t M, int32_t N, int32_t K, const void* x, in
         moe::mx_status(moe::launch_mx_quant(x, x_dtype == MOE_DTYPE_BF16, M, K, ld_x, xq, xs, nullptr, nullptr, s));
     if (st != MOE_OK) return st;
   }
-  return run_matmul(M, N, K, xq, xs, w, w_scale, out_dtype, out, ld_out, 0, s);
+  return run_matmul(M, N, K, xq, xs, w, w_scale, out_dtype, out, ld_out, 0, xs + scale_bytes(M, K), s);
 }
 
 size_t moe_mxfp4_linear_bwd_bytes(int32_t M, int32_t N, int32_t K) {
@@ -512,13 +694,14 @@ moe_status_t moe_mxfp4_linear_bwd(int32_t M, int32_t N, int32_t K, const void* d
   uint8_t* sr = qr + code_bytes(M, N);
   uint8_t* qc = sr + scale_bytes(M, N);
   uint8_t* sc = qc + code_bytes(N, M);
+  void* part = sc + scale_bytes(N, M);  // the two products take turns
   moe_status_t st = MOE_OK;
   if (dots)
     st = moe::mx_status(moe::launch_mx_quant(dy, dy_dtype == MOE_DTYPE_BF16, M, N, ld_dy, want_dx ? qr : nullptr,
                                              want_dx ? sr : nullptr, want_dw ? qc : nullptr, want_dw ? sc : nullptr, s));
-  if (st == MOE_OK && want_dx) st = run_matmul(M, K, N, qr, sr, w_col, w_col_scale, dx_dtype, dx, ld_dx, 0, s);
+  if (st == MOE_OK && want_dx) st = run_matmul(M, K, N, qr, sr, w_col, w_col_scale, dx_dtype, dx, ld_dx, 0, part, s);
   if (st == MOE_OK && want_dw)
-    st = run_matmul(N, K, M, qc, sc, x_col, x_col_scale, MOE_DTYPE_F32, dw, ld_dw, accumulate, s);
+    st = run_matmul(N, K, M, qc, sc, x_col, x_col_scale, MOE_DTYPE_F32, dw, ld_dw, accumulate, part, s);
   return st;
 }
 
