@@ -8,6 +8,7 @@ libmoe.so has not been built, importing this package raises ImportError.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -482,9 +483,10 @@ def _float_dtype(dtype, name: str) -> int:
 
 
 def _matrix(t: torch.Tensor, name: str) -> int:
-    """The dtype code of a bf16 or f32 device matrix with unit column stride
-    (and rows that do not overlap)."""
-    code = _float_dtype(t.dtype, name)
+    """The dtype code of a bf16 or f32 device matrix with unit column stride."""
+    code = _FLOAT_DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bf16 or f32")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.dim() != 2:
@@ -495,63 +497,58 @@ def _matrix(t: torch.Tensor, name: str) -> int:
 
 
 def _ld(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    rows, cols = t.shape
+    return t.stride(0) if rows > 1 else max(cols, 1)
 
 
 def _codes(q: torch.Tensor, s: torch.Tensor, rows: int, cols: int, device, name: str):
     """Checks MXFP4 codes and scales of a [rows, cols] matrix."""
-    cp = _padded(cols)
-    for t, shape, what in ((q, (rows, cp // 2), name), (s, (rows, cp // 32), name + " scales")):
-        if t.device != device or t.dtype != torch.uint8 or not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous uint8 on {device}")
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+    cp = (cols + 127) // 128 * 128
+    if (q.dtype is torch.uint8 and s.dtype is torch.uint8 and q.shape == (rows, cp // 2) and s.shape == (rows, cp // 32)
+            and q.device == device and s.device == device and q.is_contiguous() and s.is_contiguous()):
+        return
+    raise ValueError(f"{name} must be contiguous uint8 codes [{rows}, {cp // 2}] and scales [{rows}, {cp // 32}] on "
+                     f"{device}, got {q.dtype} {tuple(q.shape)} and {s.dtype} {tuple(s.shape)} on {q.device} and {s.device}")
 
 
-def _out_matrix(out, shape, dtype, device, name: str) -> torch.Tensor:
+def _out_matrix(out, rows: int, cols: int, dtype, device, name: str) -> torch.Tensor:
     """The output matrix: given (checked) or new."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty((rows, cols), dtype=dtype, device=device)
     _matrix(out, name)
-    if tuple(out.shape) != tuple(shape) or out.device != device:
-        raise ValueError(f"{name} must have shape {tuple(shape)} on {device}")
+    if out.shape != (rows, cols) or out.device != device:
+        raise ValueError(f"{name} must have shape {(rows, cols)} on {device}")
     if out.shape[0] > 1 and out.stride(0) < out.shape[1]:
         raise ValueError(f"{name} must not have overlapping rows")
     return out
 
 
-class _on:
-    """Makes `device` and, if one is given, `stream` current: outputs and
-    scratch then belong to the stream that the kernels run on.  `handle` is
-    the stream's handle.  The usual case, the current device and its current
-    stream, costs two comparisons."""
-    __slots__ = ("handle", "_ctx")
+def _elsewhere(device: torch.device, stream) -> bool:
+    """Whether a call has to make another device or stream current first."""
+    return stream is not None or device.index != torch.cuda.current_device()
 
-    def __init__(self, device: torch.device, stream):
-        index = device.index
-        if stream is None and index == torch.cuda.current_device():
-            self._ctx = None
-        elif stream is None:
-            self._ctx = torch.cuda.device(index)
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-                stream = (torch.cuda.ExternalStream(handle, device=device) if handle
-                          else torch.cuda.default_stream(device))
-            if stream.device != device:
-                raise ValueError(f"stream must be on {device}")
-            self._ctx = torch.cuda.stream(stream)
 
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        self.handle = torch.cuda.current_stream().cuda_stream
-        return self
+@contextlib.contextmanager
+def _on(device: torch.device, stream):
+    """Makes `device` and, if one is given, `stream` (a stream or its handle)
+    current: outputs and scratch then belong to the stream that the kernels
+    run on."""
+    if stream is None:
+        with torch.cuda.device(device):
+            yield
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = (torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device))
+    if stream.device != device:
+        raise ValueError(f"stream must be on {device}")
+    with torch.cuda.stream(stream):
+        yield
 
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-        return False
+
+def _current(device: torch.device) -> int:
+    """Handle of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def moe_mxfp4_quant(x: torch.Tensor, rows: bool = True, cols: bool = False, stream=None):
@@ -563,29 +560,42 @@ def moe_mxfp4_quant(x: torch.Tensor, rows: bool = True, cols: bool = False, stre
     dt = _matrix(x, "x")
     if not rows and not cols:
         raise ValueError("rows or cols must be set")
+    dev = x.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return moe_mxfp4_quant(x, rows, cols)
     R, C = x.shape
-    with _on(x.device, stream) as on:
-        new = lambda n, m: torch.empty(n, m, dtype=torch.uint8, device=x.device)
-        q_row, s_row = (new(R, _padded(C) // 2), new(R, _padded(C) // 32)) if rows else (None, None)
-        q_col, s_col = (new(C, _padded(R) // 2), new(C, _padded(R) // 32)) if cols else (None, None)
-        if R and C:
-            _check(_lib.moe_mxfp4_quant(x.data_ptr(), dt, R, C, _ld(x), q_row.data_ptr() if rows else None,
-                                        s_row.data_ptr() if rows else None, q_col.data_ptr() if cols else None,
-                                        s_col.data_ptr() if cols else None, on.handle), "moe_mxfp4_quant")
+    q_row = s_row = q_col = s_col = None
+    if rows:
+        cp = (C + 127) // 128 * 128
+        q_row = torch.empty((R, cp // 2), dtype=torch.uint8, device=dev)
+        s_row = torch.empty((R, cp // 32), dtype=torch.uint8, device=dev)
+    if cols:
+        rp = (R + 127) // 128 * 128
+        q_col = torch.empty((C, rp // 2), dtype=torch.uint8, device=dev)
+        s_col = torch.empty((C, rp // 32), dtype=torch.uint8, device=dev)
+    if R and C:
+        _check(_lib.moe_mxfp4_quant(x.data_ptr(), dt, R, C, _ld(x), q_row.data_ptr() if rows else None,
+                                    s_row.data_ptr() if rows else None, q_col.data_ptr() if cols else None,
+                                    s_col.data_ptr() if cols else None, _current(dev)), "moe_mxfp4_quant")
     return q_row, s_row, q_col, s_col
 
 
 def moe_mxfp4_dequant(q: torch.Tensor, s: torch.Tensor, cols: int, dtype: torch.dtype = torch.bfloat16,
                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The values [R, cols] that MXFP4 codes and scales stand for (exact)."""
+    dev = q.device
     if not q.is_cuda:
         raise ValueError("q must be a device tensor")
-    _codes(q, s, q.shape[0], cols, q.device, "q")
+    R = q.shape[0]
+    _codes(q, s, R, cols, dev, "q")
     _float_dtype(dtype, "dtype")
-    with _on(q.device, stream) as on:
-        out = _out_matrix(out, (q.shape[0], cols), dtype, q.device, "out")
-        _check(_lib.moe_mxfp4_dequant(q.data_ptr(), s.data_ptr(), q.shape[0], cols, _FLOAT_DTYPES[out.dtype],
-                                      out.data_ptr(), _ld(out), on.handle), "moe_mxfp4_dequant")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return moe_mxfp4_dequant(q, s, cols, dtype, out)
+    out = _out_matrix(out, R, cols, dtype, dev, "out")
+    _check(_lib.moe_mxfp4_dequant(q.data_ptr(), s.data_ptr(), R, cols, _FLOAT_DTYPES[out.dtype], out.data_ptr(), _ld(out),
+                                  _current(dev)), "moe_mxfp4_dequant")
     return out
 
 
@@ -596,21 +606,24 @@ def moe_mxfp4_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_
     is taken from the codes).  accumulate adds to a given f32 `out`."""
     if not a.is_cuda or a.dim() != 2 or b.dim() != 2:
         raise ValueError("a and b must be device matrices of codes")
+    dev = a.device
     M, N, K = a.shape[0], b.shape[0], a.shape[1] * 2
     if K % 128:
         raise ValueError("a must have rows of a multiple of 64 bytes")
-    _codes(a, a_scale, M, K, a.device, "a")
-    _codes(b, b_scale, N, K, a.device, "b")
+    _codes(a, a_scale, M, K, dev, "a")
+    _codes(b, b_scale, N, K, dev, "b")
     _float_dtype(out_dtype, "out_dtype")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    with _on(a.device, stream) as on:
-        out = _out_matrix(out, (M, N), out_dtype, a.device, "out")
-        need = _lib.moe_mxfp4_matmul_bytes(M, N, K)
-        ws = _empty_bytes(need, a.device) if need else None
-        _check(_lib.moe_mxfp4_matmul(M, N, K, a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(),
-                                     _FLOAT_DTYPES[out.dtype], out.data_ptr(), _ld(out), int(accumulate),
-                                     ws.data_ptr() if need else None, need, on.handle), "moe_mxfp4_matmul")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return moe_mxfp4_matmul(a, a_scale, b, b_scale, out_dtype, out, accumulate)
+    out = _out_matrix(out, M, N, out_dtype, dev, "out")
+    need = _lib.moe_mxfp4_matmul_bytes(M, N, K)
+    ws = _empty_bytes(need, dev) if need else None
+    _check(_lib.moe_mxfp4_matmul(M, N, K, a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(),
+                                 _FLOAT_DTYPES[out.dtype], out.data_ptr(), _ld(out), int(accumulate),
+                                 ws.data_ptr() if need else None, need, _current(dev)), "moe_mxfp4_matmul")
     return out
 
 
@@ -620,17 +633,20 @@ def moe_mxfp4_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
     """Q(x) deq(w)^T: bf16/f32 x [M, K], quantised on the way, times MXFP4
     weights w [N, K] (quantised along K)."""
     dt = _matrix(x, "x")
+    dev = x.device
     M, K = x.shape
     N = w.shape[0]
-    _codes(w, w_scale, N, K, x.device, "w")
+    _codes(w, w_scale, N, K, dev, "w")
     _float_dtype(out_dtype, "out_dtype")
-    with _on(x.device, stream) as on:
-        out = _out_matrix(out, (M, N), out_dtype, x.device, "out")
-        need = _lib.moe_mxfp4_linear_bytes(M, N, K)
-        ws = _empty_bytes(need, x.device)
-        _check(_lib.moe_mxfp4_linear(M, N, K, x.data_ptr(), dt, _ld(x), w.data_ptr(), w_scale.data_ptr(),
-                                     _FLOAT_DTYPES[out.dtype], out.data_ptr(), _ld(out), ws.data_ptr(), need,
-                                     on.handle), "moe_mxfp4_linear")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return moe_mxfp4_linear(x, w, w_scale, out_dtype, out)
+    out = _out_matrix(out, M, N, out_dtype, dev, "out")
+    need = _lib.moe_mxfp4_linear_bytes(M, N, K)
+    ws = _empty_bytes(need, dev) if need else None
+    _check(_lib.moe_mxfp4_linear(M, N, K, x.data_ptr(), dt, _ld(x), w.data_ptr(), w_scale.data_ptr(),
+                                 _FLOAT_DTYPES[out.dtype], out.data_ptr(), _ld(out), ws.data_ptr() if need else None,
+                                 need, _current(dev)), "moe_mxfp4_linear")
     return out
 
 
@@ -660,52 +676,61 @@ def moe_mxfp4_linear_bwd(dy: torch.Tensor, x_col=None, w_col=None, dx_dtype: tor
     if dw is not None and dw.dtype != torch.float32:
         raise ValueError("dw must be f32")
     _float_dtype(dx_dtype, "dx_dtype")
-    with _on(dev, stream) as on:
-        if w_col is not None:
-            dx = _out_matrix(dx, (M, K), dx_dtype, dev, "dx")
-        if x_col is not None:
-            dw = _out_matrix(dw, (N, K), torch.float32, dev, "dw")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return moe_mxfp4_linear_bwd(dy, x_col, w_col, dx_dtype, dx, dw, accumulate)
+    xp = wp = (None, None)
+    dxp = dwp = None
+    ld_dx = ld_dw = 0
+    if w_col is not None:
+        dx = _out_matrix(dx, M, K, dx_dtype, dev, "dx")
+        dxp, ld_dx, dx_dtype = dx.data_ptr(), _ld(dx), dx.dtype
+        wp = (w_col[0].data_ptr(), w_col[1].data_ptr())
+    if x_col is not None:
+        dw = _out_matrix(dw, N, K, torch.float32, dev, "dw")
+        dwp, ld_dw = dw.data_ptr(), _ld(dw)
+        xp = (x_col[0].data_ptr(), x_col[1].data_ptr())
+    if K and (M or N):
         need = _lib.moe_mxfp4_linear_bwd_bytes(M, N, K)
         ws = _empty_bytes(need, dev)
-        ptr = lambda t: t.data_ptr() if t is not None else None
-        xq, xs = x_col if x_col is not None else (None, None)
-        wq, ws_ = w_col if w_col is not None else (None, None)
-        if K and (M or N):
-            _check(_lib.moe_mxfp4_linear_bwd(M, N, K, dy.data_ptr(), dt, _ld(dy), ptr(xq), ptr(xs), ptr(wq), ptr(ws_),
-                                             _FLOAT_DTYPES[dx.dtype] if dx is not None else MOE_DTYPE_BF16, ptr(dx),
-                                             _ld(dx) if dx is not None else 0, ptr(dw),
-                                             _ld(dw) if dw is not None else 0, int(accumulate), ws.data_ptr(), need,
-                                             on.handle), "moe_mxfp4_linear_bwd")
+        _check(_lib.moe_mxfp4_linear_bwd(M, N, K, dy.data_ptr(), dt, _ld(dy), *xp, *wp, _FLOAT_DTYPES[dx_dtype], dxp, ld_dx,
+                                         dwp, ld_dw, int(accumulate), ws.data_ptr(), need, _current(dev)),
+               "moe_mxfp4_linear_bwd")
     return dx, dw
 
 
 # ---- training the router --------------------------------------------------------
 
-def _router_tensors(logits, ids, token_mask, seq_offsets, named):
-    """Checks the router's tensors; -> (T, E, k, num_seqs)."""
+def _router_tensor(t, dtype, shape, device, name: str):
+    """The address of an optional contiguous tensor, checked."""
+    if t is None:
+        return None
+    if t.dtype is not dtype and not (dtype is torch.uint8 and t.dtype is torch.bool):
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous on {device}")
+    return t.data_ptr()
+
+
+def _router_inputs(logits, ids, token_mask, seq_offsets):
+    """-> T, E, k, the number of sequences, and the addresses of the four."""
     if not logits.is_cuda or logits.dim() != 2:
         raise ValueError("logits must be a device matrix")
+    if ids.dim() != 2:
+        raise ValueError("ids must be a matrix")
     T, E = logits.shape
-    S = 1
+    k, S = ids.shape[1], 1
     if seq_offsets is not None:
         if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
             raise ValueError("seq_offsets must hold num_seqs + 1 values")
         S = seq_offsets.shape[0] - 1
-    if ids.dim() != 2:
-        raise ValueError("ids must be a matrix")
-    k = ids.shape[1]
-    for t, dtype, shape, name in ((logits, torch.float32, (T, E), "logits"), (ids, torch.int32, (T, k), "ids"),
-                                  (token_mask, (torch.uint8, torch.bool), (T,), "token_mask"),
-                                  (seq_offsets, torch.int32, (S + 1,), "seq_offsets"), *named(T, E, k, S)):
-        if t is None:
-            continue
-        if t.device != logits.device or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous on {logits.device}")
-        if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    return T, E, k, S
+    dev = logits.device
+    return T, E, k, S, (_router_tensor(logits, torch.float32, (T, E), dev, "logits"),
+                        _router_tensor(ids, torch.int32, (T, k), dev, "ids"),
+                        _router_tensor(token_mask, torch.uint8, (T,), dev, "token_mask"),
+                        _router_tensor(seq_offsets, torch.int32, (S + 1,), dev, "seq_offsets"))
 
 
 def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, token_mask: torch.Tensor | None = None,
@@ -714,20 +739,19 @@ def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, token_mask: torch.
     f32 [T, E], ids int32 [T, k], token_mask uint8/bool [T] (0: left out),
     seq_offsets int32 [S + 1] (default: one sequence of all tokens).
     -> (loss f32 [2], counts int32 [S, E], seq_tokens int32 [S + 2], lse f32 [T])."""
-    T, E, k, S = _router_tensors(logits, ids, token_mask, seq_offsets, lambda *_: ())
+    T, E, k, S, (lp, ip, mp, sp) = _router_inputs(logits, ids, token_mask, seq_offsets)
     dev = logits.device
-    with _on(dev, stream) as on:
-        loss = torch.empty(2, dtype=torch.float32, device=dev)
-        counts = torch.empty(S, E, dtype=torch.int32, device=dev)
-        seq_tokens = torch.empty(S + 2, dtype=torch.int32, device=dev)
-        lse = torch.empty(T, dtype=torch.float32, device=dev)
-        need = _lib.moe_balance_bytes(T, E, S)
-        ws = _empty_bytes(need, dev)
-        _check(_lib.moe_balance_loss(logits.data_ptr(), ids.data_ptr(), T, E, k,
-                                     token_mask.data_ptr() if token_mask is not None else None,
-                                     seq_offsets.data_ptr() if seq_offsets is not None else None, S, loss.data_ptr(),
-                                     counts.data_ptr(), seq_tokens.data_ptr(), lse.data_ptr(), ws.data_ptr(), need,
-                                     on.handle), "moe_balance_loss")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return moe_balance_loss(logits, ids, token_mask, seq_offsets)
+    loss = torch.empty(2, dtype=torch.float32, device=dev)
+    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+    seq_tokens = torch.empty(S + 2, dtype=torch.int32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    need = _lib.moe_balance_bytes(T, E, S)
+    ws = _empty_bytes(need, dev)
+    _check(_lib.moe_balance_loss(lp, ip, T, E, k, mp, sp, S, loss.data_ptr(), counts.data_ptr(), seq_tokens.data_ptr(),
+                                 lse.data_ptr(), ws.data_ptr(), need, _current(dev)), "moe_balance_loss")
     return loss, counts, seq_tokens, lse
 
 
@@ -745,18 +769,22 @@ def moe_router_bwd(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tenso
         raise ValueError("d_weights needs weights")
     if d_loss is not None and (lse is None or counts is None or seq_tokens is None):
         raise ValueError("d_loss needs lse, counts and seq_tokens")
-    T, E, k, S = _router_tensors(logits, ids, token_mask, seq_offsets, lambda T, E, k, S: (
-        (weights, torch.float32, (T, k), "weights"), (d_weights, torch.float32, (T, k), "d_weights"),
-        (lse, torch.float32, (T,), "lse"), (counts, torch.int32, (S, E), "counts"),
-        (seq_tokens, torch.int32, (S + 2,), "seq_tokens"), (d_loss, torch.float32, (2,), "d_loss"),
-        (d_logits, torch.float32, (T, E), "d_logits")))
-    ptr = lambda t: t.data_ptr() if t is not None else None
-    with _on(logits.device, stream) as on:
-        if d_logits is None:
-            d_logits = torch.empty(T, E, dtype=torch.float32, device=logits.device)
-        _check(_lib.moe_router_bwd(logits.data_ptr(), ids.data_ptr(), ptr(weights), ptr(d_weights), T, E, k,
-                                   ptr(token_mask), ptr(seq_offsets), S, ptr(lse), ptr(counts), ptr(seq_tokens),
-                                   ptr(d_loss), d_logits.data_ptr(), on.handle), "moe_router_bwd")
+    T, E, k, S, (lp, ip, mp, sp) = _router_inputs(logits, ids, token_mask, seq_offsets)
+    dev = logits.device
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return moe_router_bwd(logits, ids, weights, d_weights, lse, counts, seq_tokens, d_loss, token_mask,
+                                  seq_offsets, d_logits)
+    wp = _router_tensor(weights, torch.float32, (T, k), dev, "weights")
+    dwp = _router_tensor(d_weights, torch.float32, (T, k), dev, "d_weights")
+    ep = _router_tensor(lse, torch.float32, (T,), dev, "lse")
+    cp = _router_tensor(counts, torch.int32, (S, E), dev, "counts")
+    np_ = _router_tensor(seq_tokens, torch.int32, (S + 2,), dev, "seq_tokens")
+    dlp = _router_tensor(d_loss, torch.float32, (2,), dev, "d_loss")
+    if d_logits is None:
+        d_logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+    op = _router_tensor(d_logits, torch.float32, (T, E), dev, "d_logits")
+    _check(_lib.moe_router_bwd(lp, ip, wp, dwp, T, E, k, mp, sp, S, ep, cp, np_, dlp, op, _current(dev)), "moe_router_bwd")
     return d_logits
 
 

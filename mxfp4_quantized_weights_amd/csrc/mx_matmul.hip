@@ -19,15 +19,15 @@ namespace moe {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-// The same at any element's address: the hardware takes vector accesses that
-// are aligned to no more than their elements.
-typedef uint32_t v4u_any __attribute__((ext_vector_type(4), aligned(2)));
+// At any element's address (as v4u_any).
 typedef uint32_t v2u_any __attribute__((ext_vector_type(2), aligned(2)));
 typedef float v4f_any __attribute__((ext_vector_type(4), aligned(2)));
 
 struct MxMatmulArgs {
   const uint8_t *a, *as, *b, *bs;
-  int64_t M, N, kb;  // kb: 128-wide K blocks
+  int64_t M, N, kb;         // kb: 128-wide K blocks
+  const void* x;            // mx_few_kernel: a as values [M, K], row stride ld_x
+  int64_t K, ld_x;
   void* out;
   int64_t ld;
   int32_t accumulate;
@@ -474,6 +474,196 @@ __global__ __launch_bounds__(256) void mx_join_kernel(const float* __restrict__ 
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows (M <= 16 MB): the weights stream once past all of them.  A workgroup
+// takes 16 columns, its 8 waves every eighth 256-wide pair of K blocks each,
+// straight from memory to registers: whole 128-byte lines of 16 rows.  The
+// waves' sums meet in LDS and are added in wave order.
+//
+// In a pair, lane (r, g) holds row r's 64 values from 64 g on, the first 32 of
+// them for the first matrix instruction (the order of the sum is free as long
+// as both operands share it).
+//
+// X = 0: a is codes.  1, 2: bf16 or fp32 values, quantised on the way: a lane's
+// operand is 32 consecutive values of one row, just one group, so quantising
+// takes no exchange between lanes and the single token needs no launch of its
+// own for it.
+// ---------------------------------------------------------------------------
+constexpr int kFewWaves = 8;
+
+// A lane's 32 values of a, and their scale.
+struct FewOperand {
+  uint4 codes;
+  uint32_t scale;
+};
+template <int X>
+struct FewRaw {
+  uint4 v[X == 0 ? 1 : X == 1 ? 4 : 8];
+};
+
+// 32 values of row m from column `col` on.  WHOLE: they lie inside the row.
+template <int X, bool WHOLE>
+__device__ __forceinline__ void few_load(FewRaw<X>& f, const MxMatmulArgs& p, int64_t m, int64_t col) {
+  if constexpr (X == 0) {
+    f.v[0] = *(const uint4*)(p.a + m * p.kb * 64 + col / 2);
+  } else {
+    constexpr int V = X == 1 ? 8 : 4;  // values of sixteen bytes
+    const uint8_t* row = (const uint8_t*)p.x + (m * p.ld_x + col) * (16 / V);
+    const int left = (int)min(p.K - col, (int64_t)32);
+#pragma unroll
+    for (int i = 0; i < 32 / V; ++i) {
+      if (WHOLE || left >= V * (i + 1)) {
+        f.v[i] = mx_read16(row + 16 * i);
+      } else {
+        uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (V * i + e < left) {
+            if constexpr (X == 1)
+              u[e / 2] |= (uint32_t)((const uint16_t*)row)[V * i + e] << (16 * (e & 1));
+            else
+              u[e] = ((const uint32_t*)row)[V * i + e];
+          }
+        f.v[i] = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+    }
+  }
+}
+
+template <int X>
+__device__ __forceinline__ FewOperand few_operand(const FewRaw<X>& f, uint32_t scale) {
+  if constexpr (X == 0) {
+    return {f.v[0], scale};
+  } else if constexpr (X == 1) {
+    const uint32_t b = mx_scale_byte(
+        max(max(mx_amax_bf16(f.v[0]), mx_amax_bf16(f.v[1])), max(mx_amax_bf16(f.v[2]), mx_amax_bf16(f.v[3]))));
+    return {make_uint4(mx_codes_bf16(f.v[0], b), mx_codes_bf16(f.v[1], b), mx_codes_bf16(f.v[2], b),
+                       mx_codes_bf16(f.v[3], b)),
+            b};
+  } else {
+    uint32_t m = 0, w[4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, mx_amax_f32(f.v[i]));
+    const uint32_t b = mx_scale_byte(m);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = mx_codes_f32(f.v[2 * i], b) | mx_codes_f32(f.v[2 * i + 1], b) << 16;
+    return {make_uint4(w[0], w[1], w[2], w[3]), b};
+  }
+}
+
+__device__ __forceinline__ v4f mfma_fp4_16(const uint4& w, uint32_t ws, const FewOperand& x, v4f c) {
+  const v8i va = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+  const v8i vb = {(int)x.codes.x, (int)x.codes.y, (int)x.codes.z, (int)x.codes.w, 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, c, 4, 4, 0, (int)ws, 0, (int)x.scale);
+}
+
+// U pairs k, k + 8, ... of a wave: all loads, then the products.
+template <int X, int MB, int U>
+__device__ __forceinline__ void few_pairs(const MxMatmulArgs& p, const uint8_t* w, const uint8_t* ws, int64_t k, int r,
+                                          int g, v4f (&acc)[MB]) {
+  uint4 wv[U][2];
+  uint32_t wsc[U], xs[U][MB];
+  FewRaw<X> x[U][MB][2];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t q = k + u * kFewWaves;
+    wv[u][0] = *(const uint4*)(w + q * 128 + 32 * g);
+    wv[u][1] = *(const uint4*)(w + q * 128 + 32 * g + 16);
+    wsc[u] = *(const uint16_t*)(ws + q * 8 + 2 * g);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      const int64_t m = min((int64_t)(16 * i + r), p.M - 1);
+      if constexpr (X == 0) xs[u][i] = *(const uint16_t*)(p.as + m * p.kb * 4 + q * 8 + 2 * g);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) few_load<X, true>(x[u][i][h], p, m, q * 256 + 64 * g + 32 * h);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        acc[i] = mfma_fp4_16(wv[u][h], wsc[u] >> (8 * h), few_operand<X>(x[u][i][h], X == 0 ? xs[u][i] >> (8 * h) : 0), acc[i]);
+}
+
+template <int X, int MB, bool BF16>
+__global__ __launch_bounds__(64 * kFewWaves) void mx_few_kernel(MxMatmulArgs p) {
+  constexpr int U = X == 0 ? 4 : MB == 1 && X == 1 ? 2 : 1;  // pairs in flight per wave
+  __shared__ float part[kFewWaves][MB][16][17];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t n = min(n0 + r, p.N - 1);  // rows past the end are read again
+  const uint8_t* w = p.b + n * p.kb * 64;
+  const uint8_t* ws = p.bs + n * p.kb * 4;
+  v4f acc[MB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i) acc[i] = v4f{0, 0, 0, 0};
+  const int64_t pairs = X == 0 ? p.kb / 2 : p.K / 256;
+  int64_t k = wave;
+  for (; k + (U - 1) * kFewWaves < pairs; k += U * kFewWaves) few_pairs<X, MB, U>(p, w, ws, k, r, g, acc);
+  if constexpr (U >= 4)
+    if (k + kFewWaves < pairs) {
+      few_pairs<X, MB, 2>(p, w, ws, k, r, g, acc);
+      k += 2 * kFewWaves;
+    }
+  if (U >= 2 && k < pairs) few_pairs<X, MB, 1>(p, w, ws, k, r, g, acc);
+  // what is left past the pairs: at most two blocks, the last waves'
+  const int64_t block = 2 * pairs + (kFewWaves - 1 - wave);
+  if (block < p.kb) {
+    const uint4 wv = *(const uint4*)(w + block * 64 + 16 * g);
+    const uint32_t wsc = ws[block * 4 + g];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      const int64_t m = min((int64_t)(16 * i + r), p.M - 1);
+      FewRaw<X> x;
+      few_load<X, false>(x, p, m, block * 128 + 32 * g);
+      acc[i] = mfma_fp4_16(wv, wsc, few_operand<X>(x, X == 0 ? p.as[(m * p.kb + block) * 4 + g] : 0), acc[i]);
+    }
+  }
+  // the matrix core's last results are written before they are read
+  asm volatile("s_nop 15" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  // lane: row r of a, columns 4 g .. +4
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[wave][i][r][4 * g + j] = acc[i][j];
+  __syncthreads();
+  for (int t = threadIdx.x; t < MB * 256; t += 64 * kFewWaves) {
+    const int m = t >> 4, c = t & 15;
+    float v = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kFewWaves; ++q) v += part[q][m >> 4][m & 15][c];
+    if (m < p.M && n0 + c < p.N) {
+      const int64_t at = m * p.ld + n0 + c;
+      if constexpr (BF16)
+        ((uint16_t*)p.out)[at] = f32_to_bf16(v);
+      else
+        ((float*)p.out)[at] = p.accumulate ? ((float*)p.out)[at] + v : v;
+    }
+  }
+}
+
+// Up to 32 rows go here (2048 x 4096 weights, codes, with the quantisation of
+// x: 7.6 us at 1 row, 10.6 at 32; in 64-row tiles 10.0 and 12.2).  Up to 16 rows
+// are quantised on the way, unless every workgroup's own pass over x costs more
+// than a launch for it (us, on the way / apart: 1 x 2048 x 4096 5.3 / 7.6, 16 x
+// 2048 x 4096 7.9 / 8.9, 4 x 8192 x 4096 9.5 / 10.9; but 16 x 8192 x 4096 13.9 /
+// 12.7, 4 x 8192 x 8192 16.2 / 15.4).
+static bool mx_few_rows(int64_t M) { return M <= 32; }
+static bool mx_fused(int64_t M, int64_t N, int64_t K) { return M <= 16 && M * N * K <= 200000000; }
+
+template <int X>
+static hipError_t launch_mx_few(const MxMatmulArgs& p, bool bf16, hipStream_t s) {
+  const auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((p.N + 15) / 16)), dim3(64 * kFewWaves), 0, s, p);
+    return hipGetLastError();
+  };
+  if (p.M <= 16) return bf16 ? run(mx_few_kernel<X, 1, true>) : run(mx_few_kernel<X, 1, false>);
+  return bf16 ? run(mx_few_kernel<X, 2, true>) : run(mx_few_kernel<X, 2, false>);
+}
+
 // The tile (64 t x 64 t, t = 4, 2 or 1) and the split of K for a product.
 //
 // Time per 128-wide half, in us, with c tiles per compute unit, from sweeps of
@@ -533,6 +723,7 @@ static hipError_t launch_mx_tile(const MxMatmulArgs& p, bool bf16, hipStream_t s
 }
 
 static hipError_t launch_mx_matmul(const MxMatmulArgs& p, const MxPlan& plan, bool bf16, float* part, hipStream_t s) {
+  if (mx_few_rows(p.M)) return launch_mx_few<0>(p, bf16, s);
   if (p.kb < 4) {
     const int64_t tn = (p.N + 31) / 32, tiles = (p.M + 31) / 32 * tn, blocks = (tiles + 3) / 4;
     const dim3 grid((unsigned)(blocks < kMxMaxGrid ? blocks : kMxMaxGrid));
@@ -588,13 +779,13 @@ bool product_ok(int64_t M, int64_t N, int64_t K) {
 
 // Scratch of a product: the partial sums of a split one.
 size_t matmul_bytes(int64_t M, int64_t N, int64_t K) {
-  if (M == 0 || N == 0) return 0;
+  if (M == 0 || N == 0 || moe::mx_few_rows(M)) return 0;
   const moe::MxPlan plan = moe::mx_plan(M, N, mx_padded(K) / 128);
   return plan.pieces > 1 ? up256(plan.pieces * M * N * 4) : 0;
 }
 
-moe_status_t run_matmul(int64_t M, int64_t N, int64_t K, const void* a, const void* as, const void* b, const void* bs,
-                        int32_t out_dtype, void* out, int64_t ld_out, int32_t accumulate, void* part, hipStream_t s) {
+moe::MxMatmulArgs product_args(int64_t M, int64_t N, int64_t K, const void* a, const void* as, const void* b,
+                               const void* bs, void* out, int64_t ld_out, int32_t accumulate) {
   moe::MxMatmulArgs p{};
   p.a = (const uint8_t*)a;
   p.as = (const uint8_t*)as;
@@ -602,11 +793,19 @@ moe_status_t run_matmul(int64_t M, int64_t N, int64_t K, const void* a, const vo
   p.bs = (const uint8_t*)bs;
   p.M = M;
   p.N = N;
+  p.K = K;
   p.kb = mx_padded(K) / 128;
   p.out = out;
   p.ld = ld_out;
   p.accumulate = accumulate;
-  return moe::mx_status(moe::launch_mx_matmul(p, moe::mx_plan(M, N, p.kb), out_dtype == MOE_DTYPE_BF16, (float*)part, s));
+  return p;
+}
+
+moe_status_t run_matmul(int64_t M, int64_t N, int64_t K, const void* a, const void* as, const void* b, const void* bs,
+                        int32_t out_dtype, void* out, int64_t ld_out, int32_t accumulate, void* part, hipStream_t s) {
+  const moe::MxMatmulArgs p = product_args(M, N, K, a, as, b, bs, out, ld_out, accumulate);
+  return moe::mx_status(
+      moe::launch_mx_matmul(p, moe::mx_plan(M, N, p.kb), out_dtype == MOE_DTYPE_BF16, (float*)part, s));
 }
 
 }  // namespace
@@ -635,7 +834,8 @@ moe_status_t moe_mxfp4_matmul(int32_t M, int32_t N, int32_t K, const void* a, co
 }
 
 size_t moe_mxfp4_linear_bytes(int32_t M, int32_t N, int32_t K) {
-  return product_ok(M, N, K) ? code_bytes(M, K) + scale_bytes(M, K) + matmul_bytes(M, N, K) : 0;
+  if (!product_ok(M, N, K) || moe::mx_fused(M, N, K)) return 0;
+  return code_bytes(M, K) + scale_bytes(M, K) + matmul_bytes(M, N, K);
 }
 
 moe_status_t moe_mxfp4_linear(int32_t M, int32_t N, int32_t K, const void* x, int32_t x_dtype, int64_t ld_x,
@@ -653,6 +853,13 @@ moe_status_t moe_mxfp4_linear(int32_t M, int32_t N, int32_t K, const void* x, in
   if (need && !ws) return MOE_ERR_NULL;
   if (need && !mx_aligned(ws, 16)) return MOE_ERR_ALIGN;
   hipStream_t s = (hipStream_t)stream;
+  if (moe::mx_fused(M, N, K)) {
+    moe::MxMatmulArgs p = product_args(M, N, K, nullptr, nullptr, w, w_scale, out, ld_out, 0);
+    p.x = x;
+    p.ld_x = ld_x;
+    const bool bf16 = out_dtype == MOE_DTYPE_BF16;
+    return moe::mx_status(x_dtype == MOE_DTYPE_BF16 ? moe::launch_mx_few<1>(p, bf16, s) : moe::launch_mx_few<2>(p, bf16, s));
+  }
   uint8_t* xq = (uint8_t*)ws;
   uint8_t* xs = xq + code_bytes(M, K);
   if (K > 0) {
