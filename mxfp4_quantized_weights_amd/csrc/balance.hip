@@ -56,6 +56,27 @@ __device__ __forceinline__ int seq_offset(const int32_t* offsets, int T, int s) 
   return o < 0 ? 0 : (o > T ? T : o);
 }
 
+template <typename V>
+__device__ __forceinline__ void device_store(V* p, V v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename V>
+__device__ __forceinline__ V device_load(V* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// One expert's f P of a sequence of n valid tokens.
+__device__ __forceinline__ float balance_share(int count, float psum, int n, int E, int k) {
+  return n > 0 ? ((float)count * (float)E / ((float)k * (float)n)) * (psum / (float)n) : 0.0f;
+}
+
+__device__ __forceinline__ void balance_results(const BalanceArgs& p, float loss, float z, int n, int filled) {
+  p.loss[0] = filled ? loss / (float)filled : 0.0f;
+  p.loss[1] = n ? z / (float)n : 0.0f;
+  p.seq_tokens[p.S] = n;
+  p.seq_tokens[p.S + 1] = filled;
+}
+
 // The first sequence that ends after row t (S if none does): 64 evenly spaced
 // ends are compared at a time, one per lane.  Called by whole waves.
 __device__ __forceinline__ int seq_of(const int32_t* offsets, int T, int S, int t) {
@@ -74,36 +95,119 @@ __device__ __forceinline__ int seq_of(const int32_t* offsets, int T, int S, int 
   return lo;
 }
 
+// Wave-wide sums and maximum by row operations (quad swaps, mirrors, then the
+// rows' last lanes), read back uniformly from lane 63; the order of a sum is
+// fixed.  Lanes outside a step's rows add zero.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_or_zero(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
+}
+__device__ __forceinline__ float last_lane(float v) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
 __device__ __forceinline__ float wave_sum(float v) {
+  v += dpp_or_zero<0xB1, 0xF>(v);   // quad_perm [1,0,3,2]
+  v += dpp_or_zero<0x4E, 0xF>(v);   // quad_perm [2,3,0,1]
+  v += dpp_or_zero<0x141, 0xF>(v);  // row_half_mirror
+  v += dpp_or_zero<0x140, 0xF>(v);  // row_mirror
+  v += dpp_or_zero<0x142, 0xA>(v);  // row_bcast:15 into rows 1, 3
+  v += dpp_or_zero<0x143, 0xC>(v);  // row_bcast:31 into rows 2, 3
+  return last_lane(v);
+}
+__device__ __forceinline__ int wave_sum(int v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   return v;
 }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_or_own(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, ROWS, 0xF, false));
+}
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+  v = fmaxf(v, dpp_or_own<0xB1, 0xF>(v));
+  v = fmaxf(v, dpp_or_own<0x4E, 0xF>(v));
+  v = fmaxf(v, dpp_or_own<0x141, 0xF>(v));
+  v = fmaxf(v, dpp_or_own<0x140, 0xF>(v));
+  v = fmaxf(v, dpp_or_own<0x142, 0xA>(v));
+  v = fmaxf(v, dpp_or_own<0x143, 0xC>(v));
+  return last_lane(v);
 }
 
-// One workgroup per chunk of 64 tokens, one wave per token.  The chunk is
-// walked sequence by sequence; each (chunk, sequence) overlap leaves its sums
-// in a slot of its own (c + s: along the rows every new overlap raises c or s,
-// so no two share a slot), added up in slot order by balance_finish_kernel.
+// A token's logits in a wave: lane holds experts lane + 64 i, -inf past the
+// last.  Every load is issued (clamped into the row).
 template <int VPL>
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, float (&v)[VPL]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) v[i] = row[min(lane + 64 * i, E - 1)];
+}
+// exp(v - max), in place, with the row's maximum and sum; false if the row
+// holds nothing above -inf.  A NaN counts as something: it has to show.  exp is
+// the hardware's exp2 of (v - max) log2 e: off by |v - max| 2^-24 + 2^-23
+// relative, and the difference cannot overflow where a scaled logit could.
+template <int VPL>
+__device__ __forceinline__ bool exp_row(float (&v)[VPL], int E, float& mx, float& sum) {
+  const int lane = threadIdx.x & 63;
+  bool some = false;
+  mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    if (lane + 64 * i >= E) v[i] = -INFINITY;
+    some |= !(v[i] == -INFINITY);
+    mx = fmaxf(mx, v[i]);
+  }
+  if (!__any(some)) return false;
+  mx = wave_max(mx);
+  sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    v[i] = __builtin_amdgcn_exp2f((v[i] - mx) * 1.4426950408889634f);
+    sum += v[i];
+  }
+  sum = wave_sum(sum);
+  return true;
+}
+
+// LDS written by some lanes of a wave is read by others of the same wave: a
+// wave's LDS operations complete in order, so ordering the compiler's view is
+// all that is needed.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Rows of a wave in flight together: bounded by registers.
+constexpr int bal_rows(int vpl) { return vpl <= 5 ? 4 : vpl <= 8 ? 2 : 1; }
+
+// One workgroup per chunk of 64 tokens, one wave per token (four of them in
+// flight).  The chunk is walked sequence by sequence; each (chunk, sequence)
+// overlap leaves its sums in a slot of its own (c + s: along the rows every new
+// overlap raises c or s, so no two share a slot), added up in slot order by
+// balance_finish_kernel.  ONE: the only chunk, which writes the results itself.
+template <int VPL, bool ONE>
 __global__ __launch_bounds__(64 * kBalWaves) void balance_chunk_kernel(BalanceArgs p) {
+  constexpr int U = bal_rows(VPL);
   extern __shared__ float smem[];
   float* red = smem;                                   // [kBalWaves][E]
   int32_t* hist = (int32_t*)(red + kBalWaves * p.E);   // [E]
   __shared__ float red_z[kBalWaves];
   __shared__ int32_t red_n[kBalWaves];
+  __shared__ float red_l[kBalWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c = blockIdx.x, tb = c * kBalChunk, te = min(p.T, tb + kBalChunk);
-  if (c == 0 && tid == 0) *p.ticket = 0;
+  if (!ONE && c == 0 && tid == 0) *p.ticket = 0;
+  if (ONE)
+    for (int i = tid; i < p.S * p.E; i += 64 * kBalWaves) p.counts[i] = 0;
+  if (ONE)
+    for (int i = tid; i < p.S; i += 64 * kBalWaves) p.seq_tokens[i] = 0;
   // rows outside every sequence
   const int first = min(max(seq_offset(p.offsets, p.T, 0), tb), te);
   const int last = min(max(seq_offset(p.offsets, p.T, p.S), first), te);
   for (int t = tb + tid; t < te; t += 64 * kBalWaves)
     if (t < first || t >= last) p.lse[t] = 0.0f;
+  float one_loss = 0.0f, one_z = 0.0f;  // ONE, thread 0: sums over the sequences
+  int one_n = 0, one_filled = 0;
   int t0 = first;
   while (t0 < last) {
     const int s = p.offsets ? seq_of(p.offsets, p.T, p.S, t0) : 0;
@@ -113,40 +217,33 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_chunk_kernel(BalanceAr
     __syncthreads();
     float acc[VPL] = {}, z = 0.0f;
     int n = 0;
-    for (int t = t0 + wave; t < t1; t += kBalWaves) {
-      const float* row = p.logits + (int64_t)t * p.E;
-      float v[VPL];
+    for (int tw = t0 + wave; tw < t1; tw += U * kBalWaves) {
+      float v[U][VPL];
+      int id[U];
+      bool out[U];
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) v[i] = row[min(lane + 64 * i, p.E - 1)];
-      const int id = lane < p.k ? p.ids[(int64_t)t * p.k + lane] : -1;
-      const bool masked = p.mask && !p.mask[t];
-      float mx = -INFINITY;
-      bool some = false;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (lane + 64 * i >= p.E) v[i] = -INFINITY;
-        mx = fmaxf(mx, v[i]);
-        some |= !(v[i] == -INFINITY);  // a NaN counts: it has to show in the loss
+      for (int u = 0; u < U; ++u) {
+        const int t = min(tw + u * kBalWaves, t1 - 1);
+        load_row<VPL>(p.logits + (int64_t)t * p.E, p.E, v[u]);
+        id[u] = lane < p.k ? p.ids[(int64_t)t * p.k + lane] : -1;
+        out[u] = p.mask && !p.mask[t];
       }
-      if (masked || !__any(some)) {
-        if (lane == 0) p.lse[t] = 0.0f;
-        continue;
-      }
-      mx = wave_max(mx);
-      float ex[VPL], sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        ex[i] = expf(v[i] - mx);
-        sum += ex[i];
-      }
-      sum = wave_sum(sum);
-      const float lse = mx + logf(sum), inv = 1.0f / sum;
+      for (int u = 0; u < U; ++u) {
+        const int t = tw + u * kBalWaves;
+        if (t >= t1) break;
+        float mx, sum, lse = 0.0f;
+        if (!out[u] && exp_row<VPL>(v[u], p.E, mx, sum)) {
+          const float inv = __builtin_amdgcn_rcpf(sum);
+          lse = mx + logf(sum);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) acc[i] += ex[i] * inv;
-      z += lse * lse;
-      ++n;
-      if (lane == 0) p.lse[t] = lse;
-      if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
+          for (int i = 0; i < VPL; ++i) acc[i] += v[u][i] * inv;
+          z += lse * lse;
+          ++n;
+          if (id[u] >= 0 && id[u] < p.E) atomicAdd(&hist[id[u]], 1);
+        }
+        if (lane == 0) p.lse[t] = lse;
+      }
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
@@ -156,39 +253,60 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_chunk_kernel(BalanceAr
       red_n[wave] = n;
     }
     __syncthreads();
+    int cnt = 0;
+    z = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kBalWaves; ++w) {
+      z += red_z[w];
+      cnt += red_n[w];
+    }
     const int64_t slot = c + s;
+    float share = 0.0f;
     for (int e = tid; e < p.E; e += 64 * kBalWaves) {
       float sum = 0.0f;
+#pragma unroll
       for (int w = 0; w < kBalWaves; ++w) sum += red[w * p.E + e];
-      p.psum[slot * p.E + e] = sum;
-      p.pcount[slot * p.E + e] = hist[e];
-    }
-    if (tid == 0) {
-      float sum = 0.0f;
-      int cnt = 0;
-      for (int w = 0; w < kBalWaves; ++w) {
-        sum += red_z[w];
-        cnt += red_n[w];
+      if constexpr (ONE) {
+        p.counts[(int64_t)s * p.E + e] = hist[e];
+        share = balance_share(hist[e], sum, cnt, p.E, p.k);  // (E <= 1024: one expert per thread)
+      } else {
+        p.psum[slot * p.E + e] = sum;
+        p.pcount[slot * p.E + e] = hist[e];
       }
-      p.pz[slot] = sum;
+    }
+    if constexpr (ONE) {
+      share = wave_sum(share);
+      if (lane == 0) red_l[wave] = share;
+      __syncthreads();
+      if (tid == 0) {
+        for (int w = 0; w < kBalWaves; ++w) one_loss += red_l[w];
+        one_z += z;
+        one_n += cnt;
+        one_filled += cnt > 0;
+        p.seq_tokens[s] = cnt;
+      }
+    } else if (tid == 0) {
+      p.pz[slot] = z;
       p.pn[slot] = cnt;
     }
     __syncthreads();
     t0 = t1;
   }
+  if (ONE && tid == 0) balance_results(p, one_loss, one_z, one_n, one_filled);
 }
 
 // Workgroup (s, tile of 64 experts): adds the sequence's slots in a fixed
 // order, leaves its counts and its share of the loss; the last workgroup to
-// finish adds the shares up, again in a fixed order.
+// finish adds the shares up, again in a fixed order.  What the workgroups
+// exchange goes past the caches of their dies with stores and loads of device
+// scope, and a workgroup waits for its own stores before it takes its ticket:
+// no cache has to be written back for it.
 __global__ __launch_bounds__(64 * kBalGroups) void balance_finish_kernel(BalanceArgs p, int tiles) {
   __shared__ float rp[kBalGroups][64];
   __shared__ int32_t rc[kBalGroups][64];
-  __shared__ float rz[kBalGroups];
-  __shared__ int32_t rn[kBalGroups];
+  __shared__ float rz[kBalGroups], rl[kBalGroups];
+  __shared__ int32_t rn[kBalGroups], rf[kBalGroups];
   __shared__ int32_t is_last;
-  __shared__ float fz[kBalGroups], fl[kBalGroups];
-  __shared__ int32_t fn[kBalGroups], ff[kBalGroups];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int s = blockIdx.x / tiles, tile = blockIdx.x % tiles;
   const int e = tile * 64 + lane;
@@ -196,11 +314,27 @@ __global__ __launch_bounds__(64 * kBalGroups) void balance_finish_kernel(Balance
   const int c0 = lo / kBalChunk, c1 = lo < hi ? (hi - 1) / kBalChunk + 1 : c0;
   float sum = 0.0f;
   int cnt = 0;
-  if (e < p.E) {
-#pragma unroll 8
-    for (int c = c0 + wave; c < c1; c += kBalGroups) {
-      sum += p.psum[(int64_t)(c + s) * p.E + e];
-      cnt += p.pcount[(int64_t)(c + s) * p.E + e];
+  {
+    const float* ps = p.psum + min(e, p.E - 1);
+    const int32_t* pc = p.pcount + min(e, p.E - 1);
+    int c = c0 + wave;
+    for (; c + 7 * kBalGroups < c1; c += 8 * kBalGroups) {  // eight slots in flight
+      float a[8];
+      int32_t b[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a[i] = ps[(int64_t)(c + i * kBalGroups + s) * p.E];
+        b[i] = pc[(int64_t)(c + i * kBalGroups + s) * p.E];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum += a[i];
+        cnt += b[i];
+      }
+    }
+    for (; c < c1; c += kBalGroups) {
+      sum += ps[(int64_t)(c + s) * p.E];
+      cnt += pc[(int64_t)(c + s) * p.E];
     }
   }
   float z = 0.0f;
@@ -210,8 +344,7 @@ __global__ __launch_bounds__(64 * kBalGroups) void balance_finish_kernel(Balance
     n += p.pn[c + s];
   }
   z = wave_sum(z);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
+  n = wave_sum(n);
   rp[wave][lane] = sum;
   rc[wave][lane] = cnt;
   if (lane == 0) {
@@ -222,6 +355,7 @@ __global__ __launch_bounds__(64 * kBalGroups) void balance_finish_kernel(Balance
   if (wave == 0) {
     sum = z = 0.0f;
     cnt = n = 0;
+#pragma unroll
     for (int w = 0; w < kBalGroups; ++w) {
       sum += rp[w][lane];
       cnt += rc[w][lane];
@@ -229,61 +363,52 @@ __global__ __launch_bounds__(64 * kBalGroups) void balance_finish_kernel(Balance
       n += rn[w];
     }
     if (e < p.E) p.counts[(int64_t)s * p.E + e] = cnt;
-    float share = (n > 0 && e < p.E) ? ((float)cnt * (float)p.E / ((float)p.k * (float)n)) * (sum / (float)n) : 0.0f;
-    share = wave_sum(share);
+    const float share = wave_sum(e < p.E ? balance_share(cnt, sum, n, p.E, p.k) : 0.0f);
     if (lane == 0) {
-      p.seq_loss[(int64_t)s * tiles + tile] = share;
+      device_store(&p.seq_loss[(int64_t)s * tiles + tile], share);
       if (tile == 0) {
-        p.seq_z[s] = z;
-        p.seq_tokens[s] = n;
+        device_store(&p.seq_z[s], z);
+        device_store(&p.seq_tokens[s], n);
       }
-      __threadfence();
-      const uint32_t done = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      const uint32_t done = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       is_last = done == (uint32_t)gridDim.x - 1u;
     }
   }
   __syncthreads();
   if (!is_last) return;
-  __threadfence();
   float l = 0.0f;
   z = 0.0f;
   n = 0;
   int filled = 0;
-  for (int i = tid; i < p.S * tiles; i += 64 * kBalGroups)
-    l += __hip_atomic_load(&p.seq_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int i = tid; i < p.S * tiles; i += 64 * kBalGroups) l += device_load(&p.seq_loss[i]);
   for (int i = tid; i < p.S; i += 64 * kBalGroups) {
-    z += __hip_atomic_load(&p.seq_z[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const int ni = __hip_atomic_load(&p.seq_tokens[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    z += device_load(&p.seq_z[i]);
+    const int ni = device_load(&p.seq_tokens[i]);
     n += ni;
     filled += ni > 0;
   }
   l = wave_sum(l);
   z = wave_sum(z);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    n += __shfl_xor(n, o);
-    filled += __shfl_xor(filled, o);
-  }
+  n = wave_sum(n);
+  filled = wave_sum(filled);
   if (lane == 0) {
-    fl[wave] = l;
-    fz[wave] = z;
-    fn[wave] = n;
-    ff[wave] = filled;
+    rl[wave] = l;
+    rz[wave] = z;
+    rn[wave] = n;
+    rf[wave] = filled;
   }
   __syncthreads();
   if (tid == 0) {
     l = z = 0.0f;
     n = filled = 0;
     for (int w = 0; w < kBalGroups; ++w) {
-      l += fl[w];
-      z += fz[w];
-      n += fn[w];
-      filled += ff[w];
+      l += rl[w];
+      z += rz[w];
+      n += rn[w];
+      filled += rf[w];
     }
-    p.loss[0] = filled ? l / (float)filled : 0.0f;
-    p.loss[1] = n ? z / (float)n : 0.0f;
-    p.seq_tokens[p.S] = n;
-    p.seq_tokens[p.S + 1] = filled;
+    balance_results(p, l, z, n, filled);
   }
 }
 
@@ -302,62 +427,63 @@ struct RouterBwdArgs {
   float* d_logits;
 };
 
-// One wave per token.
+// One wave per token.  The routing weights' part is scattered over a row of
+// LDS, one per wave.
 template <int VPL>
 __global__ __launch_bounds__(256) void router_bwd_kernel(RouterBwdArgs p) {
-  const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  __shared__ float scatter[4][64 * VPL];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t = blockIdx.x * 4 + wave;
   if (t >= p.T) return;
-  const float* row = p.logits + (int64_t)t * p.E;
   float v[VPL], d[VPL] = {};
-  bool some = false;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) v[i] = row[min(lane + 64 * i, p.E - 1)];
+  load_row<VPL>(p.logits + (int64_t)t * p.E, p.E, v);
+  int id = -1;
+  float w = 0.0f, dw = 0.0f, lse = 0.0f, g0 = 0.0f, g1 = 0.0f;
+  if (p.dw && lane < p.k) {
+    id = p.ids[(int64_t)t * p.k + lane];
+    w = p.w[(int64_t)t * p.k + lane];
+    dw = p.dw[(int64_t)t * p.k + lane];
+  }
+  const bool masked = p.mask && !p.mask[t];
+  if (p.d_loss) {
+    lse = p.lse[t];
+    g0 = p.d_loss[0];
+    g1 = p.d_loss[1];
+  }
   const int s = p.offsets ? seq_of(p.offsets, p.T, p.S, t) : 0;
-  const bool inside = s < p.S && t >= seq_offset(p.offsets, p.T, 0) && !(p.mask && !p.mask[t]);
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) some |= lane + 64 * i < p.E && !(v[i] == -INFINITY);
-  if (inside && __any(some)) {
+  float mx, sum;
+  if (!masked && s < p.S && t >= seq_offset(p.offsets, p.T, 0) && exp_row<VPL>(v, p.E, mx, sum)) {
     if (p.d_loss) {
-      const float lse = p.lse[t];
-      const float n = (float)p.seq_tokens[s], N = (float)p.seq_tokens[p.S], filled = (float)p.seq_tokens[p.S + 1];
-      const float slope = p.d_loss[0] * (float)p.E / ((float)p.k * filled * n * n);
-      const float gz = p.d_loss[1] * 2.0f * lse / N;
       // p from the row's own maximum and sum: exp(l - lse) loses log E where
       // every logit is the type's lowest value
-      float pr[VPL], a[VPL], mx = -INFINITY, sum = 0.0f, dot = 0.0f;
+      const float n = (float)p.seq_tokens[s], N = (float)p.seq_tokens[p.S], filled = (float)p.seq_tokens[p.S + 1];
+      const float slope = g0 * (float)p.E / ((float)p.k * filled * n * n);
+      const int32_t* counts = p.counts + (int64_t)s * p.E;
+      float a[VPL], dot = 0.0f;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) mx = fmaxf(mx, lane + 64 * i < p.E ? v[i] : -INFINITY);
-      mx = wave_max(mx);
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        pr[i] = lane + 64 * i < p.E ? expf(v[i] - mx) : 0.0f;
-        sum += pr[i];
-      }
-      const float inv = 1.0f / wave_sum(sum);
+      for (int i = 0; i < VPL; ++i) a[i] = (float)counts[min(lane + 64 * i, p.E - 1)];
+      const float inv = __builtin_amdgcn_rcpf(sum);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        const int e = lane + 64 * i;
-        pr[i] *= inv;
-        a[i] = e < p.E ? slope * (float)p.counts[(int64_t)s * p.E + e] : 0.0f;
-        dot += pr[i] * a[i];
+        v[i] *= inv;
+        dot = fmaf(v[i], a[i], dot);
       }
-      dot = wave_sum(dot);
+      const float off = fmaf(-slope, wave_sum(dot), g1 * 2.0f * lse / N);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) d[i] = pr[i] * (a[i] - dot + gz);
+      for (int i = 0; i < VPL; ++i) d[i] = v[i] * fmaf(slope, a[i], off);
     }
     if (p.dw) {
-      const int id = lane < p.k ? p.ids[(int64_t)t * p.k + lane] : -1;
       const bool live = id >= 0 && id < p.E;
-      const float w = live ? p.w[(int64_t)t * p.k + lane] : 0.0f, dw = live ? p.dw[(int64_t)t * p.k + lane] : 0.0f;
-      const float mean = wave_sum(w * dw);
-      const float through = w * (dw - mean);
-      for (int j = 0; j < p.k; ++j) {
-        const int ej = __builtin_amdgcn_readlane(id, j);
-        const float g = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(through), j));
+      w = live ? w : 0.0f;
+      const float mean = wave_sum(live ? w * dw : 0.0f);
+      float* row = scatter[wave];
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) d[i] += ej == lane + 64 * i ? g : 0.0f;
-      }
+      for (int i = 0; i < VPL; ++i) row[lane + 64 * i] = 0.0f;
+      wave_lds_order();
+      if (live) atomicAdd(&row[id], w * (dw - mean));
+      wave_lds_order();
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) d[i] += row[lane + 64 * i];
     }
   }
 #pragma unroll
@@ -380,17 +506,17 @@ static void with_vpl(int E, F&& f) {
 static hipError_t launch_balance(const BalanceArgs& p, hipStream_t s) {
   const int tiles = (p.E + 63) / 64;
   const size_t lds = (size_t)(kBalWaves + 1) * p.E * 4;
+  const bool one = p.chunks == 1;
   hipError_t err = hipSuccess;
   with_vpl(p.E, [&](auto vpl) {
-    auto kernel = balance_chunk_kernel<decltype(vpl)::value>;
-    if (lds > 65536)
-      err = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (err == hipSuccess) {
-      hipLaunchKernelGGL(kernel, dim3(p.chunks), dim3(64 * kBalWaves), lds, s, p);
-      err = hipGetLastError();
-    }
+    constexpr int V = decltype(vpl)::value;
+    if (one)
+      hipLaunchKernelGGL((balance_chunk_kernel<V, true>), dim3(1), dim3(64 * kBalWaves), lds, s, p);
+    else
+      hipLaunchKernelGGL((balance_chunk_kernel<V, false>), dim3(p.chunks), dim3(64 * kBalWaves), lds, s, p);
+    err = hipGetLastError();
   });
-  if (err != hipSuccess) return err;
+  if (err != hipSuccess || one) return err;
   hipLaunchKernelGGL(balance_finish_kernel, dim3((unsigned)(p.S * tiles)), dim3(64 * kBalGroups), 0, s, p, tiles);
   return hipGetLastError();
 }
@@ -444,7 +570,7 @@ moe_status_t moe_balance_loss(const float* logits, const int32_t* ids, int32_t T
   p.E = E;
   p.k = top_k;
   p.S = num_seqs;
-  p.chunks = T > 0 ? (T + moe::kBalChunk - 1) / moe::kBalChunk : 1;  // without tokens: the ticket is still reset
+  p.chunks = T > 0 ? (T + moe::kBalChunk - 1) / moe::kBalChunk : 1;  // without tokens: zeros are written all the same
   p.mask = token_mask;
   p.offsets = seq_offsets;
   p.lse = lse;

@@ -713,9 +713,6 @@ static hipError_t launch_mx_tile(const MxMatmulArgs& p, bool bf16, hipStream_t s
   const uint32_t items = p.tiles_m * p.tiles_n * p.pieces;
   const dim3 grid(items);
   const auto run = [&](auto kernel) {
-    const hipError_t e =
-        hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, MxTile<MT, NT>::LDS);
-    if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, grid, dim3(256), (MxTile<MT, NT>::LDS), s, p);
     return hipGetLastError();
   };
