@@ -97,4 +97,9 @@ __device__ __forceinline__ uint32_t mx_group_max4(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x4E, 0xF, 0xF, false));  // [2,3,0,1]
 }
 
+// The value of the lane across the middle of its half row of 8.
+__device__ __forceinline__ uint32_t mx_row_half_mirror(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x141, 0xF, 0xF, false);
+}
+
 }  // namespace moe

@@ -17,9 +17,9 @@
 namespace moe {
 
 // One workgroup quantises a tile of 128 rows x TC columns (32 KB of it: TC =
-// 128 for bf16, 64 for fp32).  A thread loads 16 bytes at a time, all eight of
-// its loads in flight; a row group of 32 values is 4 (bf16) or 8 (fp32)
-// neighbouring lanes.  For the column groups the tile goes through LDS as it
+// 128 for bf16, 64 for fp32).  A thread loads 16 bytes of each of 8 rows, all of
+// them in flight; a row group of 32 values is 4 (bf16) or 8 (fp32) neighbouring
+// lanes.  For the column groups the tile goes through LDS as it
 // is, and a thread takes a dword column of it (two bf16 columns or one fp32
 // column) over 32 rows.  Codes of columns are gathered in LDS so that a
 // column's 64 bytes leave together.
@@ -78,22 +78,22 @@ __global__ __launch_bounds__(kQThreads) void mx_quant_kernel(const void* __restr
     for (int i = 0; i < PASSES; ++i) {
       const int64_t row = r0 + lr0 + RPP * i;
       if constexpr (ROW) {
-        uint32_t a = BF16 ? mx_amax_bf16(x[i]) : mx_amax_f32(x[i]);
-        a = mx_group_max4(a);
-        if (!BF16) a = max(a, (uint32_t)__builtin_amdgcn_update_dpp((int)a, (int)a, 0x141, 0xF, 0xF, false));  // row_half_mirror
-        const uint32_t b = mx_scale_byte(a);
-        // a group's codes in a lane's register: 8 of bf16, 4 of fp32
-        uint32_t w = BF16 ? mx_codes_bf16(x[i], b) : mx_codes_f32(x[i], b);
+        uint32_t b, w, sw;  // the group's scale, eight codes, the row's scale bytes of the tile
+        if constexpr (BF16) {
+          b = mx_scale_byte(mx_group_max4(mx_amax_bf16(x[i])));
+          w = mx_codes_bf16(x[i], b);
+          sw = b << (8 * (lc / 4));
+          sw |= mx_row_half_mirror(sw);
+        } else {
+          const uint32_t a = mx_group_max4(mx_amax_f32(x[i]));
+          b = mx_scale_byte(max(a, mx_row_half_mirror(a)));
+          w = mx_codes_f32(x[i], b);
+          w |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, 0xB1, 0xF, 0xF, false) << 16;  // (even lanes' are used)
+          sw = b << (8 * (lc / 8));
+        }
+        sw |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sw, 0x140, 0xF, 0xF, false);  // row_mirror
         if (row < rows) {
-          uint8_t* q = q_row + row * (cp / 2) + col / 2;
-          if constexpr (BF16)
-            *(uint32_t*)q = w;
-          else
-            *(uint16_t*)q = (uint16_t)w;
-          // the row's scale bytes of the tile: one store of four (bf16) or two (fp32)
-          uint32_t sw = 0;
-#pragma unroll
-          for (int g = 0; g < TC / 32; ++g) sw |= (uint32_t)__shfl((int)b, (t & 48) + g * (32 / V)) << (8 * g);
+          if (BF16 || lc % 2 == 0) *(uint32_t*)(q_row + row * (cp / 2) + col / 2) = w;
           if (lc == 0) {
             uint8_t* sr = s_row + row * (cp / 32) + c0 / 32;
             if constexpr (BF16)
@@ -188,48 +188,61 @@ hipError_t launch_mx_quant(const void* in, bool bf16, int64_t rows, int64_t cols
               : launch_mx_quant_t<false>(s, in, rows, cols, ld, qr, sr, qc, sc);
 }
 
-// 8 codes per thread and step.  value = E2M1 * 2^(b - 127): one or two
-// significant bits and an exponent of at least -128, exact in fp32 and in bf16
-// (whose subnormals reach 2^-133), so the bf16 form is the fp32 value's upper
-// half.  The hardware conversion gives the E2M1 value; the scale is a product
-// of its own, since its smallest results are fp32 subnormals.
+// A workgroup takes 64 rows x 128 columns, a thread 8 codes of four rows.
+// value = E2M1 * 2^(b - 127): one or two significant bits and an exponent of at
+// least -128, exact in fp32 and in bf16 (whose subnormals reach 2^-133), so the
+// bf16 form is the fp32 value's upper half.  The hardware conversion gives the
+// E2M1 value; the scale is a product of its own, since its smallest results
+// are fp32 subnormals.
+constexpr int kDqRows = 64;
 template <bool BF16>
 __global__ __launch_bounds__(256) void mx_dequant_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sc,
-                                                         int64_t units, int64_t upr, int64_t cols, int64_t cp,
+                                                         int64_t rows, int64_t cols, int64_t cp, int64_t tiles,
                                                          void* __restrict__ out, int64_t ld) {
-  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
-    const int64_t row = u / upr, col = (u - row * upr) * 8;
-    const uint32_t w = *(const uint32_t*)(q + row * (cp / 2) + col / 2);
-    const uint32_t b = sc[row * (cp / 32) + col / 32];
-    const float scale = b == 255u ? __uint_as_float(0x7FC00000u) : e8m0_value(b);
-    float v[8];
-    mx_values8(w, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= scale;
-    const int64_t at = row * ld + col;
+  const int64_t tiles_c = cp / 128;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int64_t row0 = tile / tiles_c * kDqRows + threadIdx.x / 16, col = tile % tiles_c * 128 + threadIdx.x % 16 * 8;
     const int left = (int)min(cols - col, (int64_t)8);
-    if constexpr (BF16) {
-      uint16_t* p = (uint16_t*)out + at;
-      uint32_t h[4];
+    if (left <= 0) continue;
+    uint32_t w[kDqRows / 16], b[kDqRows / 16];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        h[i] = __builtin_amdgcn_perm(__float_as_uint(v[2 * i + 1]), __float_as_uint(v[2 * i]), 0x07060302);
-      if (left == 8) {
-        mx_write16(p, make_uint4(h[0], h[1], h[2], h[3]));
+    for (int i = 0; i < kDqRows / 16; ++i) {
+      const int64_t row = min(row0 + 16 * i, rows - 1);
+      w[i] = *(const uint32_t*)(q + row * (cp / 2) + col / 2);
+      b[i] = sc[row * (cp / 32) + col / 32];
+    }
+#pragma unroll
+    for (int i = 0; i < kDqRows / 16; ++i) {
+      const int64_t row = row0 + 16 * i;
+      if (row >= rows) break;
+      const float scale = b[i] == 255u ? __uint_as_float(0x7FC00000u) : e8m0_value(b[i]);
+      float v[8];
+      mx_values8(w[i], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= scale;
+      if constexpr (BF16) {
+        uint16_t* p = (uint16_t*)out + row * ld + col;
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          h[j] = __builtin_amdgcn_perm(__float_as_uint(v[2 * j + 1]), __float_as_uint(v[2 * j]), 0x07060302);
+        if (left == 8) {
+          mx_write16(p, make_uint4(h[0], h[1], h[2], h[3]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < left) p[j] = (uint16_t)(h[j / 2] >> (16 * (j & 1)));
+        }
       } else {
+        float* p = (float*)out + row * ld + col;
+        if (left == 8) {
+          mx_write16(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+          mx_write16(p + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < left) p[i] = (uint16_t)(h[i / 2] >> (16 * (i & 1)));
-      }
-    } else {
-      float* p = (float*)out + at;
-      if (left == 8) {
-        mx_write16(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
-        mx_write16(p + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (i < left) p[i] = v[i];
+          for (int j = 0; j < 8; ++j)
+            if (j < left) p[j] = v[j];
+        }
       }
     }
   }
@@ -237,12 +250,12 @@ __global__ __launch_bounds__(256) void mx_dequant_kernel(const uint8_t* __restri
 
 static hipError_t launch_mx_dequant(const uint8_t* q, const uint8_t* sc, int64_t rows, int64_t cols, bool bf16,
                                     void* out, int64_t ld, hipStream_t s) {
-  const int64_t cp = mx_padded(cols), upr = (cols + 7) / 8, units = rows * upr, blocks = (units + 255) / 256;
-  const dim3 grid((unsigned)(blocks < kMxMaxGrid ? blocks : kMxMaxGrid));
+  const int64_t cp = mx_padded(cols), tiles = (rows + kDqRows - 1) / kDqRows * (cp / 128);
+  const dim3 grid((unsigned)(tiles < kMxMaxGrid ? tiles : kMxMaxGrid));
   if (bf16)
-    hipLaunchKernelGGL((mx_dequant_kernel<true>), grid, dim3(256), 0, s, q, sc, units, upr, cols, cp, out, ld);
+    hipLaunchKernelGGL((mx_dequant_kernel<true>), grid, dim3(256), 0, s, q, sc, rows, cols, cp, tiles, out, ld);
   else
-    hipLaunchKernelGGL((mx_dequant_kernel<false>), grid, dim3(256), 0, s, q, sc, units, upr, cols, cp, out, ld);
+    hipLaunchKernelGGL((mx_dequant_kernel<false>), grid, dim3(256), 0, s, q, sc, rows, cols, cp, tiles, out, ld);
   return hipGetLastError();
 }
 
