@@ -180,6 +180,41 @@ def test_many_tokens_and_sequences(M):
     assert abs(loss[0].item() - ref[0]) <= 4 * rel * ref[0] and abs(loss[1].item() - ref[1]) <= 4 * rel * (ref[1] + 1)
 
 
+def test_more_sequences_than_tokens(M):
+    """Sequence search over many, mostly empty, sequences, in one chunk and in several."""
+    g = torch.Generator().manual_seed(11)
+    for T, S in ((50, 9000), (300, 5000)):
+        off = torch.randint(0, T + 1, (S + 1,), generator=g).sort().values.tolist()
+        _check(M, _inputs(T, 12, 2, T), 2, None, off)
+
+
+def test_offsets_outside_the_batch_are_clamped(M):
+    lg = _inputs(100, 16, 2, 12)
+    ids, _ = M.moe_route_topk(lg, 2)
+    d = torch.tensor([1.0, 1.0], device="cuda")
+    for bad, good in (([-5, 40, 1000], [0, 40, 100]), ([200, 300], [100, 100]), ([-9, -1], [0, 0])):
+        res = []
+        for off in (bad, good):
+            off = torch.tensor(off, dtype=torch.int32, device="cuda")
+            out = M.moe_balance_loss(lg, ids, seq_offsets=off)
+            res.append(out + (M.moe_router_bwd(lg, ids, lse=out[3], counts=out[1], seq_tokens=out[2], d_loss=d, seq_offsets=off),))
+        assert all(torch.equal(a, b) for a, b in zip(*res))
+
+
+def test_binding_refusals_on_the_device(M):
+    lg = _inputs(10, 16, 2, 13)
+    ids, w = M.moe_route_topk(lg, 2)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    bad = [lambda: M.moe_balance_loss(lg, ids.long()), lambda: M.moe_balance_loss(lg.t(), ids),
+           lambda: M.moe_balance_loss(lg, ids[:5]), lambda: M.moe_balance_loss(lg, ids, token_mask=w[:, 0]),
+           lambda: M.moe_balance_loss(lg, ids, seq_offsets=i32(0)), lambda: M.moe_balance_loss(lg, ids, seq_offsets=i32(0, 10).cpu()),
+           lambda: M.moe_router_bwd(lg, ids, w, w[:5].contiguous()), lambda: M.moe_router_bwd(lg, ids, w, w.double()),
+           lambda: M.moe_router_bwd(lg, ids, w, w, d_logits=lg[:5])]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_gradient_against_differences(M):
     """Central differences of loss(logits) = 3 balance + 0.5 z + sum weights * c
     in 64 bits, selection and counts held."""

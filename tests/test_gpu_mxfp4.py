@@ -133,10 +133,34 @@ def _operand(rows, K, seed, spread=2):
     return R.pack(code).cuda(), b.to(torch.uint8).cuda(), R.values(code, b)
 
 
+def test_binding_refusals_on_the_device(M):
+    q, s, _ = _operand(8, 256, 1)
+    x = torch.zeros(4, 256, device="cuda")
+    bad = [lambda: M.moe_mxfp4_linear(x, q, s[:, :4]), lambda: M.moe_mxfp4_linear(x[:, :100], q, s),
+           lambda: M.moe_mxfp4_linear(x, q.cpu(), s), lambda: M.moe_mxfp4_linear(x.t(), q, s),
+           lambda: M.moe_mxfp4_linear(x, q, s, out=torch.zeros(4, 9, device="cuda")),
+           lambda: M.moe_mxfp4_linear(x, q, s, out=torch.zeros(1, 8, device="cuda").expand(4, 8)),
+           lambda: M.moe_mxfp4_linear(x, q, s, out_dtype=torch.float16),
+           lambda: M.moe_mxfp4_matmul(q, s, q, s, accumulate=True),
+           lambda: M.moe_mxfp4_matmul(q[:, :100].contiguous(), s, q, s),
+           lambda: M.moe_mxfp4_matmul(q[::2], s[::2], q, s), lambda: M.moe_mxfp4_dequant(q, s, 300),
+           lambda: M.moe_mxfp4_linear_bwd(x, dw=x), lambda: M.moe_mxfp4_linear_bwd(x, x_col=(q, s), dx=x),
+           lambda: M.moe_mxfp4_linear_bwd(x[:, :8], w_col=(q, s)),
+           lambda: M.moe_mxfp4_quant(x, rows=False)]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(M.MoeError):                        # rows that overlap
+        M.moe_mxfp4_quant(x[:1].expand(4, 256))
+    with pytest.raises(M.MoeError):                        # only fp32 sums accumulate
+        M.moe_mxfp4_matmul(q, s, q, s, out=torch.zeros(8, 8, dtype=BF16, device="cuda"), accumulate=True)
+
+
 SIZES = [(1, 1, 1), (1, 16, 128), (1, 2048, 4096), (3, 257, 1000), (16, 100, 160), (17, 33, 64), (31, 65, 384),
          (32, 32, 512), (33, 1000, 640), (64, 300, 2048), (65, 129, 257), (100, 288, 4096), (128, 128, 128),
          (129, 257, 896), (255, 256, 513), (288, 512, 4001), (257, 1023, 1100), (300, 4000, 1000), (513, 770, 300),
-         (1000, 130, 5000), (2, 8192, 96), (7, 31, 16000)]
+         (1000, 130, 5000), (2, 8192, 96), (7, 31, 16000), (100, 288, 300), (40, 50, 256), (33, 1000, 64),
+         (2000, 2050, 1100), (3300, 3900, 600), (3333, 3901, 513)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -173,7 +197,8 @@ def test_matmul_wide_scales(M):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("m,n,k", [(5, 33, 256), (64, 100, 512), (200, 300, 1024), (300, 520, 4096)])
+@pytest.mark.parametrize("m,n,k", [(5, 33, 256), (64, 100, 512), (50, 70, 200), (200, 300, 1024), (300, 520, 4096),
+                                   (64, 100, 4096), (2000, 2050, 512), (3300, 3900, 512)])
 def test_matmul_strided_out_and_accumulate(M, m, n, k, dtype):
     a, sa, av = _operand(m, k, 5)
     b, sb, bv = _operand(n, k, 6)
@@ -326,6 +351,36 @@ def test_products_past_32_bit_offsets(M):
     assert ((out[-100:].cpu().double() - ref).abs() <= R.product_bound(ref, mass, 200, BF16)).all()
     M.moe_mxfp4_dequant(q, s, 200, out=big[:, 2000:2200])
     assert torch.equal(big[-100:, 2000:2200].cpu().double(), R.values(code, b)[:, :200])
+
+
+def test_longest_sums(M):
+    """K = 2^24, the longest: ones times ones with a power of two per row, sums
+    that fp32 holds exactly; row offsets of up to 2 GB."""
+    K = 1 << 24
+    for m, n in ((260, 40), (3, 33)):
+        one = lambda rows: torch.full((rows, K // 2), 0x22, dtype=torch.uint8, device="cuda")   # 1.0, 1.0
+        sc = lambda rows: (120 + torch.arange(rows, device="cuda") % 9).to(torch.uint8)[:, None].expand(rows, K // 32).contiguous()
+        sa, sb = sc(m), sc(n)
+        out = M.moe_mxfp4_matmul(one(m), sa, one(n), sb, out_dtype=F32)
+        want = float(K) * torch.exp2(sa[:, :1].float() - 127) * torch.exp2(sb[:, 0].float() - 127)
+        assert torch.equal(out, want)
+
+
+def test_two_streams_at_once(M):
+    """The same products on two streams together, each with its own scratch."""
+    a, sa, _ = _operand(100, 4096, 1)
+    b, sb, _ = _operand(288, 4096, 2)
+    x = _matrix(40, 4096, BF16, 3).cuda()
+    want = M.moe_mxfp4_matmul(a, sa, b, sb), M.moe_mxfp4_linear(x, b, sb)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(20):
+        for s in streams:
+            got.append((M.moe_mxfp4_matmul(a, sa, b, sb, stream=s), M.moe_mxfp4_linear(x, b, sb, stream=s)))
+    for s in streams:
+        s.synchronize()
+    assert all(torch.equal(p, q) for g in got for p, q in zip(g, want))
 
 
 def test_other_stream_and_graph(M):

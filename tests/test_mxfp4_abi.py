@@ -2,6 +2,10 @@
 needed: every call here returns before any launch; the pointers are never
 dereferenced), scratch sizes, and the binding's own checks."""
 import ctypes
+import os
+import re
+import shutil
+import subprocess
 
 import pytest
 import torch
@@ -196,3 +200,81 @@ def test_binding_refuses_host_tensors_and_bad_arguments():
                  lambda: M.moe_router_bwd(x, q.int(), d_weights=x), lambda: M.moe_router_bwd(x, q.int(), d_loss=x)):
         with pytest.raises(ValueError):
             call()
+
+
+def _device_code(tmp_path):
+    """Instructions of each function of the built gfx950 code objects."""
+    objdump = "/opt/rocm/llvm/bin/llvm-objdump"
+    if not os.path.exists(objdump):
+        pytest.skip("LLVM tools of the ROCm install not found")
+    lib = tmp_path / "libmoe.so"
+    shutil.copy(M.LIB_PATH, lib)
+    subprocess.run([objdump, "--offloading", str(lib)], cwd=tmp_path, check=True, capture_output=True)
+    for o in sorted(p for p in tmp_path.iterdir() if "gfx950" in p.name):
+        dis = subprocess.run([objdump, "-d", "--mcpu=gfx950", str(o)], check=True, capture_output=True, text=True).stdout
+        for name, body in re.findall(r"\n[0-9a-f]+ <([^>]+)>:\n(.*?)(?=\n[0-9a-f]+ <|\Z)", dis, flags=re.S):
+            insts = [x.split("//")[0].strip() for x in body.splitlines()]
+            yield name, [x for x in insts if x and not x.endswith(":")]
+
+
+def test_direct_loads_of_the_dense_products(tmp_path):
+    """The dense products' direct loads are inline assembly the compiler cannot
+    see into.  Their scalar base must not have been written by a vector
+    instruction within the five wait states before the load, and the lanes they
+    switch off are all switched on again right after it."""
+    seen = 0
+    for name, insts in _device_code(tmp_path):
+        for i, ins in enumerate(insts):
+            m = re.match(r"global_load_lds_dwordx4 v\d+, s\[(\d+):(\d+)\]", ins)
+            if not m:
+                continue
+            seen += 1
+            base = {int(m.group(1)), int(m.group(2))}
+            assert re.match(r"s_mov_b32 exec_lo, s\d+", insts[i - 4]) and re.match(r"s_mov_b32 exec_hi, s\d+", insts[i - 3])
+            assert insts[i + 1] == "s_mov_b64 exec, -1", insts[i:i + 2]
+            states, j = 0, i - 1
+            while states < 5 and j >= 0:
+                if insts[j].startswith("s_nop"):
+                    states += int(insts[j].split()[1]) + 1
+                else:
+                    states += 1
+                    w = re.match(r"v_\w+ s(\d+),|v_\w+ s\[(\d+):(\d+)\],", insts[j])
+                    if w:
+                        lo = int(w.group(1) or w.group(2))
+                        assert not base & set(range(lo, int(w.group(3) or lo) + 1)), (name, insts[j:i + 1])
+                j -= 1
+    assert seen > 100
+
+
+def test_tile_results_read_after_their_wait_states(tmp_path):
+    """Reads of a register that a 32x32x64 FP4 product (8 passes) has written
+    come at least 16 wait states later, or after another product; the products
+    of its own accumulator chain are interlocked."""
+    def regs(spec):
+        m = re.match(r"([av])\[(\d+):(\d+)\]", spec)
+        if m:
+            return {f"{m.group(1)}{k}" for k in range(int(m.group(2)), int(m.group(3)) + 1)}
+        return {spec} if re.match(r"[av]\d+$", spec) else set()
+
+    checked = 0
+    for name, insts in _device_code(tmp_path):
+        for i, ins in enumerate(insts):
+            if not ins.startswith("v_mfma_scale_f32_32x32x64"):
+                continue
+            dst, states = regs(ins.replace(",", " ").split()[1]), 0
+            for t in insts[i + 1:i + 60]:
+                f = t.replace(",", " ").split()
+                if f[0] == "s_nop":
+                    states += int(f[1]) + 1
+                    continue
+                if f[0].startswith("v_mfma") or f[0] in ("s_endpgm", "s_branch") or f[0].startswith("s_cbranch"):
+                    if not f[0].startswith("s_cbranch"):
+                        break
+                if len(f) > 2 and dst & set().union(*[regs(x) for x in f[2:]]):
+                    assert states >= 16, (name, ins, t, states)
+                    break
+                states += 1
+                if states >= 16:
+                    break
+            checked += 1
+    assert checked > 300
