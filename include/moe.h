@@ -418,7 +418,9 @@ moe_status_t moe_mxfp4_matmul(int32_t M, int32_t N, int32_t K, const void* a, co
 /* A linear layer with MXFP4 weights: out[M, N] = Q(x) deq(w)^T, x [M, K]
  * (bf16 or f32) quantised along its rows by this call, w [N, K] quantised
  * along K.  The results are those of moe_mxfp4_quant and moe_mxfp4_matmul up
- * to the order of the fp32 sums.  ws: at least moe_mxfp4_linear_bytes. */
+ * to the order of the fp32 sums.  ws: at least moe_mxfp4_linear_bytes bytes (0,
+ * and ws may be NULL, for few rows of small products, which are quantised in
+ * registers; also 0 for invalid sizes). */
 size_t moe_mxfp4_linear_bytes(int32_t M, int32_t N, int32_t K);
 moe_status_t moe_mxfp4_linear(int32_t M, int32_t N, int32_t K, const void* x, int32_t x_dtype, int64_t ld_x,
                               const void* w, const void* w_scale, int32_t out_dtype, void* out, int64_t ld_out,
@@ -430,7 +432,7 @@ moe_status_t moe_mxfp4_linear(int32_t M, int32_t N, int32_t K, const void* x, in
  *   dw[N, K] = Q_m(dy)^T X, x_col [K, M]: x quantised along M (q_col of x),
  *              fp32, added to dw where accumulate != 0.
  * dx or dw may be NULL (then so may w_col or x_col).  ws: at least
- * moe_mxfp4_linear_bwd_bytes. */
+ * moe_mxfp4_linear_bwd_bytes bytes (0 for invalid sizes). */
 size_t moe_mxfp4_linear_bwd_bytes(int32_t M, int32_t N, int32_t K);
 moe_status_t moe_mxfp4_linear_bwd(int32_t M, int32_t N, int32_t K, const void* dy, int32_t dy_dtype, int64_t ld_dy,
                                   const void* x_col, const void* x_col_scale, const void* w_col,

@@ -469,10 +469,7 @@ def moe_forward_noalloc(cfg: MoeCfg, x: torch.Tensor, logits: torch.Tensor, w13,
 # ---- dense MXFP4 -------------------------------------------------------------
 
 _FLOAT_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
-
-
-def _padded(n: int) -> int:
-    return (n + 127) // 128 * 128
+_MAX_DIM = 1 << 24  # checked here too: a size past 32 bits would reach the library cut off
 
 
 def _float_dtype(dtype, name: str) -> int:
@@ -489,8 +486,8 @@ def _matrix(t: torch.Tensor, name: str) -> int:
         raise ValueError(f"{name} must be bf16 or f32")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be a matrix")
+    if t.dim() != 2 or max(t.shape) > _MAX_DIM:
+        raise ValueError(f"{name} must be a matrix of at most 2^24 rows and columns")
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit column stride")
     return code
@@ -513,6 +510,8 @@ def _codes(q: torch.Tensor, s: torch.Tensor, rows: int, cols: int, device, name:
 
 def _out_matrix(out, rows: int, cols: int, dtype, device, name: str) -> torch.Tensor:
     """The output matrix: given (checked) or new."""
+    if rows > _MAX_DIM or cols > _MAX_DIM:
+        raise ValueError(f"{name} must have at most 2^24 rows and columns")
     if out is None:
         return torch.empty((rows, cols), dtype=dtype, device=device)
     _matrix(out, name)
@@ -722,6 +721,8 @@ def _router_inputs(logits, ids, token_mask, seq_offsets):
         raise ValueError("ids must be a matrix")
     T, E = logits.shape
     k, S = ids.shape[1], 1
+    if max(T, E) > _MAX_DIM:
+        raise ValueError("logits must have at most 2^24 rows and 1024 columns")
     if seq_offsets is not None:
         if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
             raise ValueError("seq_offsets must hold num_seqs + 1 values")

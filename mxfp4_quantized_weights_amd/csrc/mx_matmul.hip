@@ -218,7 +218,7 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void mx_tile_kernel(MxMa
     uint32_t i = xcd * share + min(xcd, rest) + blockIdx.x / 8;
     piece = (int)(i / tiles);
     i -= piece * tiles;
-        constexpr uint32_t GM = 4;
+    constexpr uint32_t GM = 4;
     const uint32_t band = i / (GM * p.tiles_n), first = band * GM;
     const uint32_t height = min(GM, p.tiles_m - first), j = i - band * GM * p.tiles_n;
     m0 = (int64_t)(first + j % height) * T::BM;
@@ -284,12 +284,12 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void mx_tile_kernel(MxMa
   // step), stage buffer 0; scales of the current and the next group of four
   // halves.
   const int row_a = wm * MT * 32 + r, row_b = T::BM + wn * NT * 32 + r, swz = (r >> 1) & 7;
-  uint32_t ca[2][2][2], cb_[2][2][2];
+  uint32_t ca[2][2][2], cx[2][2][2];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int o = (i >> 2) * T::CODES + ((4 * ((i >> 1) & 1) + 2 * g + (i & 1)) ^ swz) * 16;
     ca[i >> 2][(i >> 1) & 1][i & 1] = row_a * 128 + o;
-    cb_[i >> 2][(i >> 1) & 1][i & 1] = row_b * 128 + o;
+    cx[i >> 2][(i >> 1) & 1][i & 1] = row_b * 128 + o;
   }
   auto group_at = [&](int q) __attribute__((always_inline)) -> uint32_t {  // offset of group q's first half in LDS
     return 2 * T::CODES + (q & 1) * T::GROUP + (4 * q - min(4 * q, kb - 4)) * 4;
@@ -303,7 +303,7 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void mx_tile_kernel(MxMa
   };
   auto read_b = [&](Frag& f, int j, int k, uint32_t sc, int part) __attribute__((always_inline)) {
     if (part < 2)
-      f.v[part] = *(const uint4*)(lds + cb_[k >> 1][k & 1][part] + j * 4096);
+      f.v[part] = *(const uint4*)(lds + cx[k >> 1][k & 1][part] + j * 4096);
     else
       f.s = *(const uint32_t*)(lds + sc + row_b * 16 + j * 512 + k * 4);
   };
@@ -475,7 +475,7 @@ __global__ __launch_bounds__(256) void mx_join_kernel(const float* __restrict__ 
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (M <= 16 MB): the weights stream once past all of them.  A workgroup
+// Few rows (M <= 16 MB <= 64): the weights stream once past all of them.  A workgroup
 // takes 16 columns, its 8 waves every eighth 256-wide pair of K blocks each,
 // straight from memory to registers: whole 128-byte lines of 16 rows.  The
 // waves' sums meet in LDS and are added in wave order.
@@ -589,7 +589,7 @@ __device__ __forceinline__ void few_pairs(const MxMatmulArgs& p, const uint8_t* 
 
 template <int X, int MB, bool BF16>
 __global__ __launch_bounds__(64 * kFewWaves) void mx_few_kernel(MxMatmulArgs p) {
-  constexpr int U = X == 0 ? 4 : MB == 1 && X == 1 ? 2 : 1;  // pairs in flight per wave
+  constexpr int U = X == 0 ? (MB <= 2 ? 4 : 2) : MB == 1 && X == 1 ? 2 : 1;  // pairs in flight per wave
   __shared__ float part[kFewWaves][MB][16][17];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * 16;
@@ -645,13 +645,21 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx_few_kernel(MxMatmulArgs p) 
   }
 }
 
-// Up to 32 rows go here (2048 x 4096 weights, codes, with the quantisation of
-// x: 7.6 us at 1 row, 10.6 at 32; in 64-row tiles 10.0 and 12.2).  Up to 16 rows
+// Up to 32 rows go here (2048 x 4096 weights, with the quantisation of x: 7.6
+// us at 1 row, 10.6 at 32; in 64-row tiles 10.0 and 12.2), and up to 64 where
+// the rows, which every workgroup reads whole, are short: then the tiles' extra
+// launch for their split sum costs as much as it saves (us, here / in tiles: 33
+// x 8192 x 4096 16.7 / 19.9, 64 x 520 x 3000 11.7 / 12.9, 64 x 4000 x 1000 8.6 /
+// 8.9, 48 x 2048 x 4096 12.5 / 12.5; 64 x 2048 x 4096 14.1 / 13.2 in a graph but
+// 14 / 17 launched one by one; 64 x 8192 x 4096, whose tiles need no split, 22.0
+// / 20.6; 33 x 1024 x 8192 15.4 / 12.4).  Up to 16 rows
 // are quantised on the way, unless every workgroup's own pass over x costs more
 // than a launch for it (us, on the way / apart: 1 x 2048 x 4096 5.3 / 7.6, 16 x
 // 2048 x 4096 7.9 / 8.9, 4 x 8192 x 4096 9.5 / 10.9; but 16 x 8192 x 4096 13.9 /
 // 12.7, 4 x 8192 x 8192 16.2 / 15.4).
-static bool mx_few_rows(int64_t M) { return M <= 32; }
+static bool mx_few_rows(int64_t M, int64_t N, int64_t K) {
+  return M <= 32 || (M <= 64 && M * K <= (N <= 4096 ? 64 : 48) * 4096);
+}
 static bool mx_fused(int64_t M, int64_t N, int64_t K) { return M <= 16 && M * N * K <= 200000000; }
 
 template <int X>
@@ -661,6 +669,10 @@ static hipError_t launch_mx_few(const MxMatmulArgs& p, bool bf16, hipStream_t s)
     return hipGetLastError();
   };
   if (p.M <= 16) return bf16 ? run(mx_few_kernel<X, 1, true>) : run(mx_few_kernel<X, 1, false>);
+  if constexpr (X == 0) {
+    if (p.M > 48) return bf16 ? run(mx_few_kernel<X, 4, true>) : run(mx_few_kernel<X, 4, false>);
+    if (p.M > 32) return bf16 ? run(mx_few_kernel<X, 3, true>) : run(mx_few_kernel<X, 3, false>);
+  }
   return bf16 ? run(mx_few_kernel<X, 2, true>) : run(mx_few_kernel<X, 2, false>);
 }
 
@@ -720,7 +732,7 @@ static hipError_t launch_mx_tile(const MxMatmulArgs& p, bool bf16, hipStream_t s
 }
 
 static hipError_t launch_mx_matmul(const MxMatmulArgs& p, const MxPlan& plan, bool bf16, float* part, hipStream_t s) {
-  if (mx_few_rows(p.M)) return launch_mx_few<0>(p, bf16, s);
+  if (mx_few_rows(p.M, p.N, p.K)) return launch_mx_few<0>(p, bf16, s);
   if (p.kb < 4) {
     const int64_t tn = (p.N + 31) / 32, tiles = (p.M + 31) / 32 * tn, blocks = (tiles + 3) / 4;
     const dim3 grid((unsigned)(blocks < kMxMaxGrid ? blocks : kMxMaxGrid));
@@ -776,7 +788,7 @@ bool product_ok(int64_t M, int64_t N, int64_t K) {
 
 // Scratch of a product: the partial sums of a split one.
 size_t matmul_bytes(int64_t M, int64_t N, int64_t K) {
-  if (M == 0 || N == 0 || moe::mx_few_rows(M)) return 0;
+  if (M == 0 || N == 0 || moe::mx_few_rows(M, N, K)) return 0;
   const moe::MxPlan plan = moe::mx_plan(M, N, mx_padded(K) / 128);
   return plan.pieces > 1 ? up256(plan.pieces * M * N * 4) : 0;
 }

@@ -209,7 +209,8 @@ def test_binding_refusals_on_the_device(M):
            lambda: M.moe_balance_loss(lg, ids[:5]), lambda: M.moe_balance_loss(lg, ids, token_mask=w[:, 0]),
            lambda: M.moe_balance_loss(lg, ids, seq_offsets=i32(0)), lambda: M.moe_balance_loss(lg, ids, seq_offsets=i32(0, 10).cpu()),
            lambda: M.moe_router_bwd(lg, ids, w, w[:5].contiguous()), lambda: M.moe_router_bwd(lg, ids, w, w.double()),
-           lambda: M.moe_router_bwd(lg, ids, w, w, d_logits=lg[:5])]
+           lambda: M.moe_router_bwd(lg, ids, w, w, d_logits=lg[:5]),
+           lambda: M.moe_balance_loss(lg.new_zeros((1 << 24) + 1, 1), ids.new_zeros((1 << 24) + 1, 1))]
     for call in bad:
         with pytest.raises(ValueError):
             call()

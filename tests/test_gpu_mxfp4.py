@@ -146,7 +146,9 @@ def test_binding_refusals_on_the_device(M):
            lambda: M.moe_mxfp4_matmul(q[::2], s[::2], q, s), lambda: M.moe_mxfp4_dequant(q, s, 300),
            lambda: M.moe_mxfp4_linear_bwd(x, dw=x), lambda: M.moe_mxfp4_linear_bwd(x, x_col=(q, s), dx=x),
            lambda: M.moe_mxfp4_linear_bwd(x[:, :8], w_col=(q, s)),
-           lambda: M.moe_mxfp4_quant(x, rows=False)]
+           lambda: M.moe_mxfp4_quant(x, rows=False),
+           lambda: M.moe_mxfp4_quant(x.new_zeros((1 << 24) + 1, 1)),
+           lambda: M.moe_mxfp4_linear(x.new_zeros(1, 0), q.new_zeros((1 << 24) + 1, 0), q.new_zeros((1 << 24) + 1, 0))]
     for call in bad:
         with pytest.raises(ValueError):
             call()
@@ -159,7 +161,8 @@ def test_binding_refusals_on_the_device(M):
 SIZES = [(1, 1, 1), (1, 16, 128), (1, 2048, 4096), (3, 257, 1000), (16, 100, 160), (17, 33, 64), (31, 65, 384),
          (32, 32, 512), (33, 1000, 640), (64, 300, 2048), (65, 129, 257), (100, 288, 4096), (128, 128, 128),
          (129, 257, 896), (255, 256, 513), (288, 512, 4001), (257, 1023, 1100), (300, 4000, 1000), (513, 770, 300),
-         (1000, 130, 5000), (2, 8192, 96), (7, 31, 16000), (100, 288, 300), (40, 50, 256), (33, 1000, 64),
+         (1000, 130, 5000), (2, 8192, 96), (7, 31, 16000), (100, 288, 300), (40, 50, 256), (33, 1000, 64), (48, 90, 4500), (63, 35, 3500),
+         (100, 70, 2683), (65, 130, 3200), (100, 200, 5188), (40, 300, 6000), (64, 64, 8200),
          (2000, 2050, 1100), (3300, 3900, 600), (3333, 3901, 513)]
 
 
@@ -198,7 +201,7 @@ def test_matmul_wide_scales(M):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("m,n,k", [(5, 33, 256), (64, 100, 512), (50, 70, 200), (200, 300, 1024), (300, 520, 4096),
-                                   (64, 100, 4096), (2000, 2050, 512), (3300, 3900, 512)])
+                                   (64, 100, 4096), (60, 70, 5120), (2000, 2050, 512), (3300, 3900, 512)])
 def test_matmul_strided_out_and_accumulate(M, m, n, k, dtype):
     a, sa, av = _operand(m, k, 5)
     b, sb, bv = _operand(n, k, 6)
