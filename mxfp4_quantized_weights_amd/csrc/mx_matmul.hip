@@ -43,6 +43,14 @@ __device__ __forceinline__ uint32_t mx_bf16x2(float a, float b) {
   return __builtin_bit_cast(uint32_t, h);
 }
 
+// The same, where it stands: the compiler gathers plain conversions of a tile's
+// accumulators in one place, and their results then do not fit the registers.
+__device__ __forceinline__ uint32_t mx_bf16x2_here(float a, float b) {
+  uint32_t h;
+  asm("v_cvt_pk_bf16_f32 %0, %1, %2" : "=v"(h) : "v"(a), "v"(b));
+  return h;
+}
+
 // LDS written by some lanes of a wave is read by others of the same wave: a
 // wave's LDS operations complete in order, so ordering the compiler's view is
 // all that is needed.
@@ -56,9 +64,9 @@ __device__ __forceinline__ void mx_wave_lds_sync() {
 // Lane l holds row l % 32 of both operands, 32 values of the sum; the result
 // lane l holds C[8 (i / 4) + 4 (l / 32) + i % 4][l % 32], i = 0..15.
 template <int OP>
-__device__ __forceinline__ v16f mfma_fp4_32(const uint4& a, const uint4& b, v16f c, uint32_t sa, uint32_t sb) {
-  const v8i va = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-  const v8i vb = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+__device__ __forceinline__ v16f mfma_fp4_32(const v4u& a, const v4u& b, v16f c, uint32_t sa, uint32_t sb) {
+  const v8i va = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const v8i vb = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(va, vb, c, 4, 4, OP, (int)sa, OP, (int)sb);
 }
 
@@ -91,8 +99,10 @@ struct MxTile {
   static constexpr int CHUNKS = ROWS / 8 / 4;         // 1 KB loads (8 rows) per wave and stage
   static constexpr int SCALES = (ROWS / 64 + 3) / 4;  // 1 KB scale loads (64 rows) per wave and two stages
   static constexpr int BUFFERS = 2 * (CODES + GROUP);
-  static constexpr int LDS = BUFFERS + 64;            // scale reads past the last half reach up to 40 bytes over
-  static_assert(ROWS % 128 == 0 && BUFFERS >= 4 * 4096, "load split; room for the turned rows");
+  static constexpr bool WALKS = MT >= 4;              // a workgroup computes several tiles, one after the other
+  static constexpr int TURN = WALKS ? BUFFERS : 0;    // where the results are turned: 4 KB per wave
+  static constexpr int LDS = WALKS ? BUFFERS + 16384 : BUFFERS + 64;  // (scale reads past the last half reach up to 40 bytes over)
+  static_assert(MT == NT && BUFFERS >= 16384 && LDS <= 163840, "waves 0, 1 load a's codes, 2, 3 b's; room for the turned rows");
 };
 
 #pragma clang diagnostic push
@@ -108,15 +118,34 @@ __device__ __forceinline__ const uint8_t* mx_uniform(const uint8_t* p) {
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(u >> 32));
   return (const uint8_t*)((uint64_t)hi << 32 | lo);
 }
-// 16 bytes per lane (none where `lanes` is 0, else -1) from base + off to LDS at lds + 16 * lane.  Every
-// lane of the wave is active here, before and after.
-__device__ __forceinline__ void mx_dma16(const uint8_t* base, uint32_t off, uint32_t lds, int lanes) {
+// 16 bytes per lane from base + off to LDS at lds + at + 16 * lane.  (The sum is
+// formed here: as a value of its own each load's would be kept in a register.)
+__device__ __forceinline__ void mx_dma16(const uint8_t* base, uint32_t off, uint32_t lds, int at) {
+  uint32_t to;
+  asm volatile("s_add_u32 %0, %3, %4\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               : "=&s"(to)
+               : "v"(off), "s"(mx_uniform(base)), "s"(__builtin_amdgcn_readfirstlane(lds)), "i"(at)
+               : "memory", "m0", "scc");
+}
+// The same for all lanes or none (`lanes` -1 or 0).  Every lane of the wave is
+// active here, before and after.
+__device__ __forceinline__ void mx_dma16_if(const uint8_t* base, uint32_t off, uint32_t lds, int at, int lanes) {
+  uint32_t to;
   asm volatile(
-      "s_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1\n\ts_mov_b64 exec, -1" ::"v"(off),
-      "s"(mx_uniform(base)), "s"(__builtin_amdgcn_readfirstlane(lds)), "s"(__builtin_amdgcn_readfirstlane(lanes))
-      : "memory", "m0");
+      "s_add_u32 %0, %3, %4\n\ts_mov_b32 exec_lo, %5\n\ts_mov_b32 exec_hi, %5\n\ts_mov_b32 m0, %0\n\ts_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1"
+      : "=&s"(to)
+      : "v"(off), "s"(mx_uniform(base)), "s"(__builtin_amdgcn_readfirstlane(lds)), "i"(at),
+        "s"(__builtin_amdgcn_readfirstlane(lanes))
+      : "memory", "m0", "scc");
 }
 #pragma clang diagnostic pop
+
+// From LDS at byte address at + off (off folds into the instruction).
+template <typename V>
+__device__ __forceinline__ V lds_read(uint32_t at, int off) {
+  return *(const __attribute__((address_space(3))) V*)((const __attribute__((address_space(3))) uint8_t*)(uintptr_t)at + off);
+}
 
 // Everything this wave has loaded and read has arrived, then all waves meet.
 __device__ __forceinline__ void mx_wait_barrier() {
@@ -127,7 +156,9 @@ __device__ __forceinline__ void mx_wait_barrier() {
 // [M, N] (row stride ld).  Blocks of 32 rows x 128 bytes are turned in 4 KB of
 // the wave's own LDS from the lanes' runs of four columns into whole rows:
 // 16-byte unit c of row r lies in place c ^ (r % 8), so that neither side's
-// accesses collide.
+// accesses collide.  Whole tiles take at least MT * NT * 64 lanes' * 16 bytes
+// of results / 1 KB = kStores store instructions, and nothing waits for them;
+// else everything has been written on return.
 template <int MT, int NT, bool BF16>
 __device__ __forceinline__ void mx_write_tile(const v16f (&acc)[MT][NT], uint8_t* turn, void* out, int64_t ld, bool accumulate,
                                               int64_t m0, int64_t n0, int64_t M, int64_t N) {
@@ -135,67 +166,90 @@ __device__ __forceinline__ void mx_write_tile(const v16f (&acc)[MT][NT], uint8_t
   constexpr int W = NT * 32 * E < 128 ? NT * 32 * E : 128;  // bytes of a block's row
   constexpr int JN = W / E / 32;                   // 32-column tiles of a block
   constexpr int UNITS = W / 16, ROWS = 64 / UNITS, LOADS = 32 / ROWS;  // a load: ROWS rows, 1 KB
+  constexpr int BLOCKS = MT * NT / JN;
   static_assert(ROWS % UNITS == 0, "the rotation is the same in every load");
-  const uint32_t lane = threadIdx.x & 63;
-  const int64_t stride = ld;
+  uint32_t lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));  // the addresses are worked out here, not kept in registers from tile to tile
   const uint32_t r = lane & 31, g = lane >> 5;
   const uint32_t row0 = lane / UNITS, c0 = lane % UNITS;
   const int rows = (int)min((int64_t)32 * MT, M - m0), cols = (int)min((int64_t)32 * NT, N - n0);
-  if (rows <= 0 || cols <= 0) return;
-  uint8_t* const base = (uint8_t*)out + (m0 * ld + n0) * E;
-  const bool whole = cols == 32 * NT && rows == 32 * MT;
+  uint8_t* to = (uint8_t*)out + ((m0 + row0) * ld + n0) * E + c0 * 16;  // the lane's units, block by block
+  const uint8_t* from = turn + (row0 * UNITS + (c0 ^ (row0 & (UNITS - 1)))) * 16;
+  const int64_t step = ROWS * E * ld;
+  typedef typename std::conditional<BF16, uint2, float4>::type Run;  // four columns
+  auto pack = [&](int b, Run (&v)[JN * 4]) __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
+    for (int q = 0; q < JN * 4; ++q) {
+      const v16f& a = acc[b * JN / NT][b * JN % NT + q / 4];
+      const int e = 4 * (q % 4);
+      if constexpr (BF16)
+        v[q] = make_uint2(mx_bf16x2_here(a[e], a[e + 1]), mx_bf16x2_here(a[e + 2], a[e + 3]));
+      else
+        v[q] = make_float4(a[e], a[e + 1], a[e + 2], a[e + 3]);
+    }
+  };
+  auto put = [&](const Run (&v)[JN * 4]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j0 = 0; j0 < NT; j0 += JN) {
+    for (int q = 0; q < JN * 4; ++q) {
+      if constexpr (BF16)
+        *(uint2*)(turn + (r * UNITS + (q ^ (r & (UNITS - 1)))) * 16 + 8 * g) = v[q];
+      else
+        *(float4*)(turn + (r * UNITS + ((2 * q + g) ^ (r & (UNITS - 1)))) * 16) = v[q];
+    }
+    mx_wave_lds_sync();
+  };
+  const bool whole = cols == 32 * NT && rows == 32 * MT && (BF16 || !accumulate);
+  Run v[JN * 4];
+  pack(0, v);
 #pragma unroll
-      for (int j = j0; j < j0 + JN; ++j)
+  for (int b = 0; b < BLOCKS; ++b) {
+    put(v);
+    v4u x[LOADS];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const v16f& a = acc[i][j];
-          if constexpr (BF16)
-            *(uint2*)(turn + (r * UNITS + (((j - j0) * 4 + q) ^ (r & (UNITS - 1)))) * 16 + 8 * g) =
-                make_uint2(mx_bf16x2(a[4 * q], a[4 * q + 1]), mx_bf16x2(a[4 * q + 2], a[4 * q + 3]));
-          else
-            *(float4*)(turn + (r * UNITS + (((j - j0) * 8 + 2 * q + g) ^ (r & (UNITS - 1)))) * 16) =
-                make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
-        }
-      mx_wave_lds_sync();
-      const uint8_t* from = turn + (row0 * UNITS + (c0 ^ (row0 & (UNITS - 1)))) * 16;
-      uint8_t* to = base + (int64_t)(i * 32 + row0) * stride * E + j0 * 32 * E + c0 * 16;
-      if (whole && (BF16 || !accumulate)) {
-        v4u x[LOADS];
+    for (int t = 0; t < LOADS; ++t) x[t] = *(const v4u*)(from + t * 1024);
+    if (b + 1 < BLOCKS) pack(b + 1, v);  // while the rows are read
+    uint8_t* o = to + b * JN % NT * 32 * E;
+    if (whole) {
 #pragma unroll
-        for (int t = 0; t < LOADS; ++t) x[t] = *(const v4u*)(from + t * 1024);
-#pragma unroll
-        for (int t = 0; t < LOADS; ++t) __builtin_nontemporal_store(x[t], (v4u_any*)(to + (int64_t)t * ROWS * E * stride));
-      } else {
-        const int left = cols - j0 * 32 - (int)c0 * (16 / E);  // columns from the lane's first on
-#pragma unroll
-        for (int t = 0; t < LOADS; ++t) {
-          if (i * 32 + (int)row0 + t * ROWS >= rows || left <= 0) continue;
-          uint8_t* o = to + (int64_t)t * ROWS * E * stride;
-          const uint8_t* x = from + t * 1024;
-          if (left >= 16 / E) {
-            v4f v = *(const v4f*)x;
-            if (!BF16 && accumulate) {
-              v += *(const v4f_any*)o;
-            }
-            *(v4f_any*)o = v;
-          } else {
+      for (int t = 0; t < LOADS; ++t) __builtin_nontemporal_store(x[t], (v4u_any*)(o + t * step));
+    } else {
+      const int left = cols - b * JN % NT * 32 - (int)c0 * (16 / E);  // columns from the lane's first on
 #pragma unroll 1
-            for (int e = 0; e < left; ++e) {
-              if constexpr (BF16)
-                ((uint16_t*)o)[e] = ((const uint16_t*)x)[e];
-              else
-                ((float*)o)[e] = (accumulate ? ((float*)o)[e] : 0.0f) + ((const float*)x)[e];
-            }
+      for (int t = 0; t < LOADS; ++t, o += step) {
+        if (b * JN / NT * 32 + (int)row0 + t * ROWS >= rows || left <= 0) continue;
+        const uint8_t* y = from + t * 1024;
+        if (left >= 16 / E) {
+          v4f w = *(const v4f*)y;
+          if (!BF16 && accumulate) {
+            w += *(const v4f_any*)o;
+          }
+          *(v4f_any*)o = w;
+        } else {
+#pragma unroll 1
+          for (int e = 0; e < left; ++e) {
+            if constexpr (BF16)
+              ((uint16_t*)o)[e] = ((const uint16_t*)y)[e];
+            else
+              ((float*)o)[e] = (accumulate ? ((float*)o)[e] : 0.0f) + ((const float*)y)[e];
           }
         }
       }
-      mx_wave_lds_sync();
-      __builtin_amdgcn_sched_barrier(0);
     }
+    if ((b + 1) * JN % NT == 0) to += LOADS * step;
+    mx_wave_lds_sync();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (!whole) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+template <int V>
+using Int = std::integral_constant<int, V>;
+// f(Int<0>) .. f(Int<N - 1>)
+template <int N, typename F>
+__device__ __forceinline__ void mx_for(F&& f) {
+  if constexpr (N > 0) {
+    mx_for<N - 1>(f);
+    f(Int<N - 1>{});
   }
 }
 
@@ -207,130 +261,164 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void mx_tile_kernel(MxMa
   const int r = lane & 31, g = lane >> 5;
   const int wm = wave >> 1, wn = wave & 1;
 
-  // The workgroup's tile and its piece of K.  Workgroups go round the 8 XCDs:
-  // each XCD gets a contiguous part of the list of (piece, tile) items, in
-  // which runs of GM tile rows share their b columns.
+  // The workgroup's tiles and their pieces of K.  Workgroups go round the 8
+  // XCDs: each XCD gets a contiguous part of the list of (piece, tile) items,
+  // in which runs of GM tile rows share their b columns.
+  const uint32_t tiles = p.tiles_m * p.tiles_n, total = tiles * p.pieces;
+  const uint32_t xcd = blockIdx.x % 8, share = total / 8, rest = total % 8;
+  const uint32_t last_item = (xcd + 1) * share + min(xcd + 1, rest);
+  const uint32_t stride = gridDim.x / 8 + (xcd < gridDim.x % 8);  // workgroups on this XCD
+  uint32_t item = xcd * share + min(xcd, rest) + blockIdx.x / 8;
   int64_t m0, n0;
-  int piece;
-  {
-    const uint32_t tiles = p.tiles_m * p.tiles_n, total = tiles * p.pieces;
-    const uint32_t xcd = blockIdx.x % 8, share = total / 8, rest = total % 8;
-    uint32_t i = xcd * share + min(xcd, rest) + blockIdx.x / 8;
-    piece = (int)(i / tiles);
-    i -= piece * tiles;
+  int piece, kb, stages;
+  const uint8_t *codes, *scales;
+  auto locate = [&]() __attribute__((always_inline)) {
+    piece = (int)(item / tiles);
+    const uint32_t i = item - piece * tiles;
     constexpr uint32_t GM = 4;
     const uint32_t band = i / (GM * p.tiles_n), first = band * GM;
     const uint32_t height = min(GM, p.tiles_m - first), j = i - band * GM * p.tiles_n;
     m0 = (int64_t)(first + j % height) * T::BM;
     n0 = (int64_t)(j / height) * T::BN;
-  }
-  const int64_t kb0 = (int64_t)piece * p.piece_kb;
-  const int kb = __builtin_amdgcn_readfirstlane((int)min(p.piece_kb, p.kb - kb0));  // 128-wide halves of this workgroup
-  const int stages = (kb + 1) / 2;
-  const uint8_t* base_a = mx_uniform(p.a + (m0 * p.kb + kb0) * 64);
-  const uint8_t* base_b = mx_uniform(p.b + (n0 * p.kb + kb0) * 64);
-  const uint8_t* base_as = mx_uniform(p.as + (m0 * p.kb + kb0) * 4);
-  const uint8_t* base_bs = mx_uniform(p.bs + (n0 * p.kb + kb0) * 4);
+    const int64_t kb0 = (int64_t)piece * p.piece_kb;
+    kb = __builtin_amdgcn_readfirstlane((int)min(p.piece_kb, p.kb - kb0));  // 128-wide halves of this item
+    stages = (kb + 1) / 2;
+    codes = mx_uniform(wave < 2 ? p.a + (m0 * p.kb + kb0) * 64 : p.b + (n0 * p.kb + kb0) * 64);
+    scales = mx_uniform(min(wave * T::SCALES, T::ROWS / 64 - 1) * 64 < T::BM ? p.as + (m0 * p.kb + kb0) * 4
+                                                                             : p.bs + (n0 * p.kb + kb0) * 4);
+  };
   // Source offsets of this wave's loads, from the tile's first row.  Rows past
   // the matrix are read as its last row; their results are not stored.
-  const int rows_a = (int)min((int64_t)T::BM, p.M - m0), rows_b = (int)min((int64_t)T::BN, p.N - n0);
   uint32_t off[T::CHUNKS], soff[T::SCALES];
+  auto offsets = [&]() __attribute__((always_inline)) {
+    int at = lane;
+    asm volatile("" : "+v"(at));  // as in mx_write_tile
+    const int rows_a = (int)min((int64_t)T::BM, p.M - m0), rows_b = (int)min((int64_t)T::BN, p.N - n0);
 #pragma unroll
-  for (int q = 0; q < T::CHUNKS; ++q) {
-    const int row = (wave * T::CHUNKS + q) * 8 + (lane >> 3);
-    const uint32_t in = row < T::BM ? min(row, rows_a - 1) : min(row - T::BM, rows_b - 1);
-    off[q] = in * (uint32_t)p.kb * 64u + (((lane & 7) ^ ((row >> 1) & 7)) * 16);
-  }
+    for (int q = 0; q < T::CHUNKS; ++q) {
+      const int row = (wave * T::CHUNKS + q) * 8 + (at >> 3);
+      const uint32_t in = row < T::BM ? min(row, rows_a - 1) : min(row - T::BM, rows_b - 1);
+      off[q] = in * (uint32_t)p.kb * 64u + (((at & 7) ^ ((row >> 1) & 7)) * 16);
+    }
 #pragma unroll
-  for (int q = 0; q < T::SCALES; ++q) {
-    const int row = min(wave * T::SCALES + q, T::ROWS / 64 - 1) * 64 + lane;
-    const uint32_t in = row < T::BM ? min(row, rows_a - 1) : min(row - T::BM, rows_b - 1);
-    soff[q] = in * (uint32_t)p.kb * 4u;
-  }
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
-
-  // Load x of stage st.  In a last stage of one half (`single`) the other
-  // half's bytes lie past the row: the first half is loaded twice, and the
-  // second not used.  A lane's piece lies in the second half where bit 2 of
-  // its slot differs from bit 2 of the rotation, which is bit 0 of the chunk.
-  auto issue1 = [&](int st, int x, uint32_t back0, uint32_t back1, int lanes, bool even) __attribute__((always_inline)) {
-    if (x < T::CHUNKS) {
-      const int c = wave * T::CHUNKS + x;
-      mx_dma16((c * 8 < T::BM ? base_a : base_b) + (int64_t)st * 128, off[x] - (c & 1 ? back1 : back0),
-               lds0 + (st & 1) * T::CODES + c * 1024, lanes);
-    } else if (even) {
-      // scales come for four halves at a time, the last four of the row where
-      // fewer are left
-      const int q = x - T::CHUNKS, c = min(wave * T::SCALES + q, T::ROWS / 64 - 1);
-      mx_dma16((c * 64 < T::BM ? base_as : base_bs) + (int64_t)min(2 * st, kb - 4) * 4, soff[q],
-               lds0 + 2 * T::CODES + ((st >> 1) & 1) * T::GROUP + c * 1024, lanes);
+    for (int q = 0; q < T::SCALES; ++q) {
+      const int row = min(wave * T::SCALES + q, T::ROWS / 64 - 1) * 64 + at;
+      const uint32_t in = row < T::BM ? min(row, rows_a - 1) : min(row - T::BM, rows_b - 1);
+      soff[q] = in * (uint32_t)p.kb * 4u;
     }
   };
-  auto issue = [&](int st) __attribute__((always_inline)) {
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)lds);
+
+  // Load x of stage st (par = st % 2).  In a last stage of one half the other
+  // half's bytes lie past the row: the first half is loaded twice, and the
+  // second not used.  A lane's piece lies in the second half where bit 2 of
+  // its slot differs from bit 2 of the rotation, which is bit 0 of the chunk:
+  // back0 and back1 take it back there.  IF: only where `lanes` is -1.
+  auto issue1 = [&](auto masked, int st, auto par_, auto x_, uint32_t back0, uint32_t back1, int lanes)
+                    __attribute__((always_inline)) {
+    constexpr int x = decltype(x_)::value, par = decltype(par_)::value;
+    const auto load = [&](const uint8_t* base, uint32_t from, uint32_t to, auto at) __attribute__((always_inline)) {
+      if constexpr (decltype(masked)::value)
+        mx_dma16_if(base, from, to, decltype(at)::value, lanes);
+      else
+        mx_dma16(base, from, to, decltype(at)::value);
+    };
+    if constexpr (x < T::CHUNKS) {
+      load(codes + (int64_t)st * 128, off[x] - (x & 1 ? back1 : back0), lds0 + wave * (T::CHUNKS * 2048),
+           Int<x * 2048 + par * 1024>{});
+    } else if constexpr (!par) {
+      // scales come for four halves at a time, the last four of the row where
+      // fewer are left
+      const int c = min(wave * T::SCALES + x - T::CHUNKS, T::ROWS / 64 - 1);
+      load(scales + (int64_t)min(2 * st, kb - 4) * 4, soff[x - T::CHUNKS],
+           lds0 + 2 * T::CODES + ((st >> 1) & 1) * T::GROUP + c * 1024, Int<0>{});
+    }
+  };
+  auto issue = [&](int st, auto par, auto loads) __attribute__((always_inline)) {
     const bool single = 2 * st + 1 >= kb;
     const uint32_t back0 = single ? (lane & 4) << 4 : 0, back1 = single ? (~lane & 4) << 4 : 0;
-#pragma unroll
-    for (int x = 0; x < T::CHUNKS + T::SCALES; ++x) issue1(st, x, back0, back1, -1, !(st & 1));
+    mx_for<decltype(loads)::value>([&](auto x) __attribute__((always_inline)) {
+      issue1(std::false_type{}, st, par, x, back0, back1, -1);
+    });
   };
 
   v16f acc[MT][NT];
   // Fragments of a 128-wide half (two 64-wide steps).
   struct Frag {
-    uint4 v[2];
+    v4u v[2];
     uint32_t s;
   };
   Frag fb[2][NT], fa[MT + 1];
   // Addresses of the lane's first a and b row: codes by (half of a stage,
-  // step), stage buffer 0; scales of the current and the next group of four
-  // halves.
+  // step), stage buffer 0.
   const int row_a = wm * MT * 32 + r, row_b = T::BM + wn * NT * 32 + r, swz = (r >> 1) & 7;
-  uint32_t ca[2][2][2], cx[2][2][2];
+  uint32_t ca[2][2], cx[2][2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int o = (i >> 2) * T::CODES + ((4 * ((i >> 1) & 1) + 2 * g + (i & 1)) ^ swz) * 16;
-    ca[i >> 2][(i >> 1) & 1][i & 1] = row_a * 128 + o;
-    cx[i >> 2][(i >> 1) & 1][i & 1] = row_b * 128 + o;
+  for (int i = 0; i < 4; ++i) {
+    const int o = ((4 * (i >> 1) + 2 * g + (i & 1)) ^ swz) * 16;
+    ca[i >> 1][i & 1] = lds0 + row_a / 8 * 2048 + row_a % 8 * 128 + o;
+    cx[i >> 1][i & 1] = lds0 + row_b / 8 * 2048 + row_b % 8 * 128 + o;
+    asm("" : "+v"(ca[i >> 1][i & 1]), "+v"(cx[i >> 1][i & 1]));  // kept, not worked out anew for every read
   }
+  uint32_t scale_a = row_a * 16 + 2 * g, scale_b = row_b * 16 + 2 * g;
+  asm("" : "+v"(scale_a), "+v"(scale_b));
   auto group_at = [&](int q) __attribute__((always_inline)) -> uint32_t {  // offset of group q's first half in LDS
-    return 2 * T::CODES + (q & 1) * T::GROUP + (4 * q - min(4 * q, kb - 4)) * 4;
+    return lds0 + 2 * T::CODES + (q & 1) * T::GROUP + (4 * q - min(4 * q, kb - 4)) * 4;
   };
   // part 0, 1: the steps' codes; 2: the scales.  k: half within its group of four.
   auto read_a = [&](Frag& f, int i, int k, uint32_t sc, int part) __attribute__((always_inline)) {
     if (part < 2)
-      f.v[part] = *(const uint4*)(lds + ca[k >> 1][k & 1][part] + i * 4096);
+      f.v[part] = lds_read<v4u>(ca[k & 1][part], (k >> 1) * 1024 + i * 8192);
     else
-      f.s = *(const uint32_t*)(lds + sc + row_a * 16 + i * 512 + k * 4);
+      f.s = lds_read<uint16_t>(sc + scale_a, i * 512 + k * 4);
   };
   auto read_b = [&](Frag& f, int j, int k, uint32_t sc, int part) __attribute__((always_inline)) {
     if (part < 2)
-      f.v[part] = *(const uint4*)(lds + cx[k >> 1][k & 1][part] + j * 4096);
+      f.v[part] = lds_read<v4u>(cx[k & 1][part], (k >> 1) * 1024 + j * 8192);
     else
-      f.s = *(const uint32_t*)(lds + sc + row_b * 16 + j * 512 + k * 4);
+      f.s = lds_read<uint16_t>(sc + scale_b, j * 512 + k * 4);
   };
+  // at least so many stores lie between a tile's first loads and its first wait
+  constexpr int kStores = T::WALKS ? (BF16 ? MT * NT * 2 : 63) : 0;
   constexpr int kMfma = 2 * MT * NT;
   constexpr int kPub = MT >= 2 ? (MT - 2) * NT * 2 : 0;  // the instruction before which stages change hands
   constexpr int kSlots = kMfma - kPub;
-  constexpr int kReadSlots = kSlots * 3 / 4;  // the reads, a little ahead of their use; the loads over all of them
-  // Half k of group q.  Halves past the end are multiplied with scales of
+  constexpr int kReadSlots = kSlots * 3 / 4;  // the reads, a little ahead of their use
+  // The loads of a stage: kOdd of them in the half that frees its buffer, the
+  // others over most of the next.  Of the large tiles the second half takes
+  // half: a load's 64 addresses keep the compute unit's one address path busy
+  // for half a matrix instruction, and four waves share it (16384 x 8192 x
+  // 4096: all in the first half 299 us, split 289).
+  constexpr int kLoads = T::CHUNKS + T::SCALES;
+  constexpr int kOdd = MT >= 4 ? kLoads / 2 : kLoads, kEvenSlots = kMfma * 3 / 4;
+  // Half k of group q.  LAST: one of the last groups, some of whose halves or
+  // loads may lie past the end.  Such halves are multiplied with scales of
   // 2^-127 on both sides, whose products vanish in fp32.
-  auto half = [&](int q, int k, uint32_t sc, uint32_t sc_next, Frag (&cb)[NT], Frag (&nb)[NT]) __attribute__((always_inline)) {
-    const int u = 4 * q + k;
-    const uint32_t width = u < kb ? 16 : 0;
+  auto half = [&](auto last, auto first, int q, auto k_, uint32_t sc, uint32_t sc_next, Frag (&cb)[NT], Frag (&nb)[NT]) __attribute__((always_inline)) {
+    constexpr bool LAST = decltype(last)::value, FIRST = decltype(first)::value;
+    constexpr int k = decltype(k_)::value;
+    const uint32_t live = 4 * q + k < kb ? 0xFFFF : 0;
     uint32_t sb[NT], sa = 0;
-    const int st = (u >> 1) + 2;
+    constexpr Int<k == 0 || k == 3> par;  // the stage being loaded
+    const int st = 2 * q + (k == 0 ? 1 : k == 3 ? 3 : 2);
     const bool more = st < stages, single = 2 * st + 1 >= kb;
     uint32_t back0 = 0, back1 = 0;
 #pragma unroll
     for (int n = 0; n < kMfma; ++n) {
       const int i = n / (2 * NT), t = n % (2 * NT), j = t % NT;
       if (n == kPub && (k & 1)) {
-        mx_wait_barrier();
+        if (FIRST && k == 1)
+          asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kStores) : "memory");
+        else
+          mx_wait_barrier();
+      }
+      if (LAST && ((k & 1) ? n == kPub : (kOdd < kLoads && n == 0))) {
         back0 = single ? (lane & 4) << 4 : 0;
         back1 = single ? (~lane & 4) << 4 : 0;
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (t == 0) sa = __builtin_amdgcn_ubfe(fa[i].s, 16 * g, width);
-      if (i == 0 && t < NT) sb[j] = __builtin_amdgcn_ubfe(cb[j].s, 16 * g, width);
+      if (t == 0) sa = LAST ? fa[i].s & live : fa[i].s;
+      if (i == 0 && t < NT) sb[j] = LAST ? cb[j].s & live : cb[j].s;
       if (t < NT)
         acc[i][j] = mfma_fp4_32<0>(cb[j].v[0], fa[i].v[0], acc[i][j], sb[j], sa);
       else
@@ -351,29 +439,32 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void mx_tile_kernel(MxMa
           else
             read_b(nb[x / 3 - 1], x / 3 - 1, (k + 1) & 3, k == 3 ? sc_next : sc, 2 - x % 3);
         }
-      if ((k & 1) && n >= kPub) {
-        constexpr int kL = T::CHUNKS + T::SCALES;
-#pragma unroll
-        for (int x = 0; x < kL; ++x)
-          if (kPub + x * kSlots / kL == n) issue1(st, x, back0, back1, more ? -1 : 0, k == 1);
-      }
+      mx_for<kLoads>([&](auto x) __attribute__((always_inline)) {
+        constexpr bool now = x < kOdd;  // in the half that frees the buffer
+        if (now ? (k & 1) && kPub + x * kSlots / kOdd == n
+                : !(k & 1) && !(FIRST && k == 0) && (x - kOdd) * kEvenSlots / (kLoads - kOdd + now) == n)
+          issue1(last, st, par, x, back0, back1, more ? -1 : 0);
+      });
     }
     __builtin_amdgcn_sched_barrier(0);
     fa[0] = fa[MT];
   };
 
-  if (kb > 0) issue(0);
-  if (stages > 1) issue(1);
+  locate();
+  offsets();
+  issue(0, Int<0>{}, Int<kLoads>{});
+  if (stages > 1) issue(1, Int<1>{}, Int<T::WALKS ? kLoads : kOdd>{});
+  // stage 0 has arrived; of stage 1's loads any may still be under way
+  if (stages > 1 && !T::WALKS)
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(T::CHUNKS) : "memory");
+  else
+    mx_wait_barrier();
+#pragma unroll 1
+  for (;;) {
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = v16f{};
-  if (kb > 0) {
-    // stage 0 has arrived; of stage 1's loads any may still be under way
-    if (stages > 1)
-      asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(T::CHUNKS) : "memory");
-    else
-      mx_wait_barrier();
+      for (int j = 0; j < NT; ++j) acc[i][j] = v16f{};
     uint32_t sc = group_at(0);
 #pragma unroll
     for (int x = 0; x < 3; ++x) {
@@ -381,24 +472,47 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void mx_tile_kernel(MxMa
       for (int j = 0; j < NT; ++j) read_b(fb[0][j], j, 0, sc, x);
       read_a(fa[0], 0, 0, sc, x);
     }
-#pragma unroll 1
-    for (int q = 0; 4 * q < kb; ++q) {
+    int q = 0;
+    auto group = [&](auto last, auto first) __attribute__((always_inline)) {
       const uint32_t sc_next = group_at(q + 1);
-      half(q, 0, sc, sc_next, fb[0], fb[1]);
-      half(q, 1, sc, sc_next, fb[1], fb[0]);
-      half(q, 2, sc, sc_next, fb[0], fb[1]);
-      half(q, 3, sc, sc_next, fb[1], fb[0]);
+      half(last, first, q, Int<0>{}, sc, sc_next, fb[0], fb[1]);
+      half(last, first, q, Int<1>{}, sc, sc_next, fb[1], fb[0]);
+      half(last, first, q, Int<2>{}, sc, sc_next, fb[0], fb[1]);
+      half(last, first, q, Int<3>{}, sc, sc_next, fb[1], fb[0]);
       sc = sc_next;
+      ++q;
+    };
+    if constexpr (T::WALKS) group(std::true_type{}, std::true_type{});
+    // a group loads up to the stage of halves 4 q + 6 and 4 q + 7
+#pragma unroll 1
+    while (4 * q + 8 <= kb) group(std::false_type{}, std::false_type{});
+#pragma unroll 1
+    while (4 * q < kb) group(std::true_type{}, std::false_type{});
+    // every wave is done with the stage buffers; the matrix core's last results
+    // are written before they are read
+    mx_wait_barrier();
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    const int64_t mw = m0 + wm * MT * 32, nw = n0 + wn * NT * 32;
+    uint8_t* const out = (uint8_t*)p.out + piece * p.piece_bytes;
+    bool again = false;
+    if constexpr (T::WALKS) {
+      item += stride;
+      again = item < last_item;
+      if (again) {
+        locate();
+        offsets();
+        issue(0, Int<0>{}, Int<kLoads>{});
+        if (stages > 1) issue(1, Int<1>{}, Int<kLoads>{});
+      }
     }
+    mx_write_tile<MT, NT, BF16>(acc, lds + T::TURN + wave * 4096, out, p.ld, p.accumulate, mw, nw, p.M, p.N);
+    if (!again) break;
+    offsets();  // (not kept while the results are on their way out)
+    // stage 0 of the next tile; its other loads and the stores may still be under way
+    constexpr int kLate = T::CHUNKS + kStores < 63 ? T::CHUNKS + kStores : 63;
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLate) : "memory");
   }
-  // every wave is done with the stage buffers, which the tile goes through on
-  // its way out; the matrix core's last results are written before they are
-  // read
-  mx_wait_barrier();
-  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-  mx_write_tile<MT, NT, BF16>(acc, lds + wave * 4096, (uint8_t*)p.out + piece * p.piece_bytes, p.ld, p.accumulate,
-                              m0 + wm * MT * 32, n0 + wn * NT * 32, p.M, p.N);
 }
 
 // Sums of fewer than four 128-wide blocks, too short for the stages above: one
@@ -416,8 +530,8 @@ __global__ __launch_bounds__(256) void mx_short_kernel(MxMatmulArgs p, int64_t t
     v16f c = {};
     for (int64_t k = 0; k < p.kb; ++k) {
       const uint32_t sa = *(const uint32_t*)(psa + k * 4) >> (16 * g), sb = *(const uint32_t*)(psb + k * 4) >> (16 * g);
-      const uint4 a0 = *(const uint4*)(pa + k * 64), a1 = *(const uint4*)(pa + k * 64 + 16);
-      const uint4 b0 = *(const uint4*)(pb + k * 64), b1 = *(const uint4*)(pb + k * 64 + 16);
+      const v4u a0 = *(const v4u*)(pa + k * 64), a1 = *(const v4u*)(pa + k * 64 + 16);
+      const v4u b0 = *(const v4u*)(pb + k * 64), b1 = *(const v4u*)(pb + k * 64 + 16);
       c = mfma_fp4_32<0>(b0, a0, c, sb, sa);
       c = mfma_fp4_32<1>(b1, a1, c, sb, sa);
     }
@@ -723,7 +837,8 @@ static MxPlan mx_plan(int64_t M, int64_t N, int64_t kb) {
 template <int MT, int NT>
 static hipError_t launch_mx_tile(const MxMatmulArgs& p, bool bf16, hipStream_t s) {
   const uint32_t items = p.tiles_m * p.tiles_n * p.pieces;
-  const dim3 grid(items);
+  // one workgroup per compute unit that walks, else one per item
+  const dim3 grid(MxTile<MT, NT>::WALKS && items > 256 ? 256 : items);
   const auto run = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(256), (MxTile<MT, NT>::LDS), s, p);
     return hipGetLastError();

@@ -220,9 +220,9 @@ def _device_code(tmp_path):
 def test_direct_loads_of_the_dense_products(tmp_path):
     """The dense products' direct loads are inline assembly the compiler cannot
     see into.  Their scalar base must not have been written by a vector
-    instruction within the five wait states before the load, and the lanes they
-    switch off are all switched on again right after it."""
-    seen = 0
+    instruction within the five wait states before the load, and the lanes that
+    some of them switch off are all switched on again right after."""
+    seen = masked = 0
     for name, insts in _device_code(tmp_path):
         for i, ins in enumerate(insts):
             m = re.match(r"global_load_lds_dwordx4 v\d+, s\[(\d+):(\d+)\]", ins)
@@ -230,8 +230,10 @@ def test_direct_loads_of_the_dense_products(tmp_path):
                 continue
             seen += 1
             base = {int(m.group(1)), int(m.group(2))}
-            assert re.match(r"s_mov_b32 exec_lo, s\d+", insts[i - 4]) and re.match(r"s_mov_b32 exec_hi, s\d+", insts[i - 3])
-            assert insts[i + 1] == "s_mov_b64 exec, -1", insts[i:i + 2]
+            if "exec_hi" in insts[i - 3]:
+                masked += 1
+                assert re.match(r"s_mov_b32 exec_lo, s\d+", insts[i - 4]) and re.match(r"s_mov_b32 exec_hi, s\d+", insts[i - 3])
+                assert insts[i + 1] == "s_mov_b64 exec, -1", insts[i:i + 2]
             states, j = 0, i - 1
             while states < 5 and j >= 0:
                 if insts[j].startswith("s_nop"):
@@ -243,7 +245,7 @@ def test_direct_loads_of_the_dense_products(tmp_path):
                         lo = int(w.group(1) or w.group(2))
                         assert not base & set(range(lo, int(w.group(3) or lo) + 1)), (name, insts[j:i + 1])
                 j -= 1
-    assert seen > 100
+    assert seen > 2 * masked > 100
 
 
 def test_tile_results_read_after_their_wait_states(tmp_path):
