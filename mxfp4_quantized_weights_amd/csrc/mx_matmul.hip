@@ -381,7 +381,10 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void mx_tile_kernel(MxMa
   // at least so many stores lie between a tile's first loads and its first wait
   constexpr int kStores = T::WALKS ? (BF16 ? MT * NT * 2 : 63) : 0;
   constexpr int kMfma = 2 * MT * NT;
-  constexpr int kPub = MT >= 2 ? (MT - 2) * NT * 2 : 0;  // the instruction before which stages change hands
+  // The instruction before which stages change hands.  The second half's a
+  // tiles 1 .. MT-1 are read before it: what is read after it, other waves' loads
+  // may already be writing over.
+  constexpr int kPub = MT == 1 ? 0 : MT == 2 ? 4 : (MT - 2) * NT * 2;
   constexpr int kSlots = kMfma - kPub;
   constexpr int kReadSlots = kSlots * 3 / 4;  // the reads, a little ahead of their use
   // The loads of a stage: kOdd of them in the half that frees its buffer, the
@@ -426,6 +429,7 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void mx_tile_kernel(MxMa
       __builtin_amdgcn_sched_barrier(0);
       // a tiles 1 .. MT-1: all before kPub
       constexpr int kA = 3 * (MT - 1), kSlotsA = kPub > 0 ? kPub - 1 : 1;
+      static_assert(kA == 0 || (kA - 1) * kSlotsA / kA < kPub, "read before the stage's buffer is given away");
 #pragma unroll
       for (int x = 0; x < kA; ++x)
         if (x * kSlotsA / (kA > 0 ? kA : 1) == n) read_a(fa[1 + x / 3], 1 + x / 3, k, sc, 2 - x % 3);

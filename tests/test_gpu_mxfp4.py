@@ -356,6 +356,20 @@ def test_products_past_32_bit_offsets(M):
     assert torch.equal(big[-100:, 2000:2200].cpu().double(), R.values(code, b)[:, :200])
 
 
+@pytest.mark.parametrize("m,n,k", [(2000, 2050, 1100), (3300, 3900, 600), (1000, 1000, 700), (4097, 4100, 520)])
+def test_repeated_runs_give_the_same_bits(M, m, n, k):
+    """Many runs one behind the other: a load that overtook a read of what it
+    writes over would show in some of them."""
+    a, sa, _ = _operand(m, k, 1)
+    b, sb, _ = _operand(n, k, 2)
+    want = M.moe_mxfp4_matmul(a, sa, b, sb, out_dtype=F32)
+    outs = [torch.empty_like(want) for _ in range(10)]
+    for _ in range(10):
+        for o in outs:
+            M.moe_mxfp4_matmul(a, sa, b, sb, out=o)
+        assert all(torch.equal(o, want) for o in outs)
+
+
 def test_longest_sums(M):
     """K = 2^24, the longest: ones times ones with a power of two per row, sums
     that fp32 holds exactly; row offsets of up to 2 GB."""
