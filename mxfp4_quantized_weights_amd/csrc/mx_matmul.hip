@@ -454,6 +454,12 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void mx_tile_kernel(MxMa
     fa[0] = fa[MT];
   };
 
+  // Workgroups that walk start apart: else all write their results at the same
+  // time, and all wait for memory with idle matrix cores (16384 x 8192 x 4096:
+  // 271 us together, 260 spread over 18000 cycles, 264 over 46000; 16384 x 4096
+  // x 2048: 84, 79, 89).
+  if (T::WALKS && total > gridDim.x)
+    for (uint32_t i = 0; i < blockIdx.x / 8; ++i) __builtin_amdgcn_s_sleep(9);  // 576 cycles
   locate();
   offsets();
   issue(0, Int<0>{}, Int<kLoads>{});
