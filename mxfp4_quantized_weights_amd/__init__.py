@@ -493,6 +493,11 @@ def _matrix(t: torch.Tensor, name: str) -> int:
     return code
 
 
+def _new(rows: int, cols: int, dtype, device) -> torch.Tensor:
+    """A new matrix (by strides: 1.4 us of the host's time, torch.empty 1.7)."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
+
+
 def _ld(t: torch.Tensor) -> int:
     rows, cols = t.shape
     return t.stride(0) if rows > 1 else max(cols, 1)
@@ -513,7 +518,7 @@ def _out_matrix(out, rows: int, cols: int, dtype, device, name: str) -> torch.Te
     if rows > _MAX_DIM or cols > _MAX_DIM:
         raise ValueError(f"{name} must have at most 2^24 rows and columns")
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=device)
+        return _new(rows, cols, dtype, device)
     _matrix(out, name)
     if out.shape != (rows, cols) or out.device != device:
         raise ValueError(f"{name} must have shape {(rows, cols)} on {device}")
@@ -567,12 +572,12 @@ def moe_mxfp4_quant(x: torch.Tensor, rows: bool = True, cols: bool = False, stre
     q_row = s_row = q_col = s_col = None
     if rows:
         cp = (C + 127) // 128 * 128
-        q_row = torch.empty((R, cp // 2), dtype=torch.uint8, device=dev)
-        s_row = torch.empty((R, cp // 32), dtype=torch.uint8, device=dev)
+        q_row = _new(R, cp // 2, torch.uint8, dev)
+        s_row = _new(R, cp // 32, torch.uint8, dev)
     if cols:
         rp = (R + 127) // 128 * 128
-        q_col = torch.empty((C, rp // 2), dtype=torch.uint8, device=dev)
-        s_col = torch.empty((C, rp // 32), dtype=torch.uint8, device=dev)
+        q_col = _new(C, rp // 2, torch.uint8, dev)
+        s_col = _new(C, rp // 32, torch.uint8, dev)
     if R and C:
         _check(_lib.moe_mxfp4_quant(x.data_ptr(), dt, R, C, _ld(x), q_row.data_ptr() if rows else None,
                                     s_row.data_ptr() if rows else None, q_col.data_ptr() if cols else None,
@@ -745,14 +750,15 @@ def moe_balance_loss(logits: torch.Tensor, ids: torch.Tensor, token_mask: torch.
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return moe_balance_loss(logits, ids, token_mask, seq_offsets)
-    loss = torch.empty(2, dtype=torch.float32, device=dev)
-    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
-    seq_tokens = torch.empty(S + 2, dtype=torch.int32, device=dev)
-    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    loss = torch.empty_strided((2,), (1,), dtype=torch.float32, device=dev)
+    counts = _new(S, E, torch.int32, dev)
+    seq_tokens = torch.empty_strided((S + 2,), (1,), dtype=torch.int32, device=dev)
+    lse = torch.empty_strided((T,), (1,), dtype=torch.float32, device=dev)
     need = _lib.moe_balance_bytes(T, E, S)
-    ws = _empty_bytes(need, dev)
+    ws = _empty_bytes(need, dev) if need else None
     _check(_lib.moe_balance_loss(lp, ip, T, E, k, mp, sp, S, loss.data_ptr(), counts.data_ptr(), seq_tokens.data_ptr(),
-                                 lse.data_ptr(), ws.data_ptr(), need, _current(dev)), "moe_balance_loss")
+                                 lse.data_ptr(), ws.data_ptr() if need else None, need, _current(dev)),
+           "moe_balance_loss")
     return loss, counts, seq_tokens, lse
 
 
@@ -783,7 +789,7 @@ def moe_router_bwd(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tenso
     np_ = _router_tensor(seq_tokens, torch.int32, (S + 2,), dev, "seq_tokens")
     dlp = _router_tensor(d_loss, torch.float32, (2,), dev, "d_loss")
     if d_logits is None:
-        d_logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        d_logits = _new(T, E, torch.float32, dev)
     op = _router_tensor(d_logits, torch.float32, (T, E), dev, "d_logits")
     _check(_lib.moe_router_bwd(lp, ip, wp, dwp, T, E, k, mp, sp, S, ep, cp, np_, dlp, op, _current(dev)), "moe_router_bwd")
     return d_logits

@@ -547,7 +547,7 @@ bool aligned4(const void* p) { return (uintptr_t)p % 4 == 0; }
 extern "C" {
 
 size_t moe_balance_bytes(int32_t T, int32_t E, int32_t num_seqs) {
-  if (!sizes_ok(T, E, 1, num_seqs)) return 0;
+  if (!sizes_ok(T, E, 1, num_seqs) || T <= moe::kBalChunk) return 0;  // one workgroup keeps its sums to itself
   const int64_t slots = (T + moe::kBalChunk - 1) / moe::kBalChunk + (int64_t)num_seqs;
   return 2 * up256(slots * E * 4) + 2 * up256(slots * 4) + up256((int64_t)num_seqs * ((E + 63) / 64) * 4) +
          up256((int64_t)num_seqs * 4) + 256;
@@ -558,11 +558,12 @@ moe_status_t moe_balance_loss(const float* logits, const int32_t* ids, int32_t T
                               int32_t* counts, int32_t* seq_tokens, float* lse, void* ws, size_t ws_bytes,
                               void* stream) {
   if (!sizes_ok(T, E, top_k, num_seqs) || (!seq_offsets && num_seqs != 1)) return MOE_ERR_SHAPE;
-  if (!loss || !counts || !seq_tokens || !ws || (T > 0 && (!logits || !ids || !lse))) return MOE_ERR_NULL;
+  const size_t need = moe_balance_bytes(T, E, num_seqs);
+  if (!loss || !counts || !seq_tokens || (need && !ws) || (T > 0 && (!logits || !ids || !lse))) return MOE_ERR_NULL;
   if (!aligned4(logits) || !aligned4(ids) || !aligned4(seq_offsets) || !aligned4(loss) || !aligned4(counts) ||
       !aligned4(seq_tokens) || !aligned4(lse) || (uintptr_t)ws % 16)
     return MOE_ERR_ALIGN;
-  if (ws_bytes < moe_balance_bytes(T, E, num_seqs)) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
   moe::BalanceArgs p{};
   p.logits = logits;
   p.ids = ids;
@@ -577,6 +578,7 @@ moe_status_t moe_balance_loss(const float* logits, const int32_t* ids, int32_t T
   p.counts = counts;
   p.seq_tokens = seq_tokens;
   p.loss = loss;
+  if (!need) return moe::launch_balance(p, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
   const int64_t slots = (T + moe::kBalChunk - 1) / moe::kBalChunk + (int64_t)num_seqs;
   uint8_t* w = (uint8_t*)ws;
   p.psum = (float*)w; w += up256(slots * E * 4);

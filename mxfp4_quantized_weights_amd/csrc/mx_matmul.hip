@@ -561,8 +561,9 @@ __global__ __launch_bounds__(256) void mx_short_kernel(MxMatmulArgs p, int64_t t
 
 // out (+)= the pieces' sums, added in piece order.
 template <bool BF16>
-__global__ __launch_bounds__(256) void mx_join_kernel(const float* __restrict__ part, int pieces, int64_t M, int64_t N,
-                                                      void* out, int64_t ld, int accumulate) {
+__global__ __launch_bounds__(256) void mx_join_kernel(const float* __restrict__ part, MxMatmulArgs p) {
+  const int64_t M = p.M, N = p.N, ld = p.ld;
+  const int pieces = (int)p.pieces;
   const int64_t groups = (N + 3) / 4, total = M * groups;
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
     const int64_t m = u / groups, n = (u - m * groups) * 4;
@@ -577,7 +578,7 @@ __global__ __launch_bounds__(256) void mx_join_kernel(const float* __restrict__ 
         for (int i = 0; i < left; ++i) v[i] += src[(int64_t)k * M * N + i];
     }
     if constexpr (BF16) {
-      uint16_t* o = (uint16_t*)out + m * ld + n;
+      uint16_t* o = (uint16_t*)p.out + m * ld + n;
       const uint32_t h0 = mx_bf16x2(v[0], v[1]), h1 = mx_bf16x2(v[2], v[3]);
       if (left == 4) {
         *(v2u_any*)o = v2u_any{h0, h1};
@@ -587,12 +588,12 @@ __global__ __launch_bounds__(256) void mx_join_kernel(const float* __restrict__ 
         if (left > 2) o[2] = (uint16_t)h1;
       }
     } else {
-      float* o = (float*)out + m * ld + n;
+      float* o = (float*)p.out + m * ld + n;
       if (left == 4) {
-        if (accumulate) v += *(const v4f_any*)o;
+        if (p.accumulate) v += *(const v4f_any*)o;
         *(v4f_any*)o = v;
       } else {
-        for (int i = 0; i < left; ++i) o[i] = accumulate ? o[i] + v[i] : v[i];
+        for (int i = 0; i < left; ++i) o[i] = p.accumulate ? o[i] + v[i] : v[i];
       }
     }
   }
@@ -886,11 +887,12 @@ static hipError_t launch_mx_matmul(const MxMatmulArgs& p, const MxPlan& plan, bo
   if (e != hipSuccess || !split) return e;
   const int64_t blocks = (p.M * ((p.N + 3) / 4) + 255) / 256;
   const dim3 grid((unsigned)(blocks < kMxMaxGrid ? blocks : kMxMaxGrid));
+  MxMatmulArgs j = p;
+  j.pieces = plan.pieces;
   if (bf16)
-    hipLaunchKernelGGL(mx_join_kernel<true>, grid, dim3(256), 0, s, part, plan.pieces, p.M, p.N, p.out, p.ld, 0);
+    hipLaunchKernelGGL(mx_join_kernel<true>, grid, dim3(256), 0, s, part, j);
   else
-    hipLaunchKernelGGL(mx_join_kernel<false>, grid, dim3(256), 0, s, part, plan.pieces, p.M, p.N, p.out, p.ld,
-                       p.accumulate);
+    hipLaunchKernelGGL(mx_join_kernel<false>, grid, dim3(256), 0, s, part, j);
   return hipGetLastError();
 }
 

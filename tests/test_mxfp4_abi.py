@@ -155,6 +155,7 @@ def test_balance_refusals():
         return f(*a)
 
     assert need > 0 and M.lib().moe_balance_bytes(-1, 288, 1) == 0 and M.lib().moe_balance_bytes(1, 1025, 1) == 0
+    assert M.lib().moe_balance_bytes(64, 288, 3) == 0 and M.lib().moe_balance_bytes(65, 288, 3) > 0
     assert M.lib().moe_balance_bytes(1, 8, 0) == 0 and M.lib().moe_balance_bytes(1, 8, 65537) == 0
     for i, bad in ((2, (-1, 1 << 22)), (3, (0, 7, 1025)), (4, (0, 17)), (7, (0, 65537))):
         for v in bad:
