@@ -500,6 +500,7 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void mx_tile_kernel(MxMa
     while (4 * q < kb) group(std::true_type{}, std::false_type{});
     // every wave is done with the stage buffers; the matrix core's last results
     // are written before they are read
+    __builtin_amdgcn_sched_barrier(0);
     mx_wait_barrier();
     asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
@@ -525,37 +526,44 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void mx_tile_kernel(MxMa
   }
 }
 
-// Sums of fewer than four 128-wide blocks, too short for the stages above: one
-// wave per 32 x 32 tile, operands straight from memory.
-template <bool BF16>
+// Sums of KB < 4 128-wide blocks, too short for the stages above: a 64 x 64
+// tile per wave, all of its operands straight from memory at once.
+template <int KB, bool BF16>
 __global__ __launch_bounds__(256) void mx_short_kernel(MxMatmulArgs p, int64_t tiles_n, int64_t tiles) {
-  const int lane = threadIdx.x & 63, r = lane & 31, g = lane >> 5;
-  for (int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); tile < tiles; tile += (int64_t)gridDim.x * 4) {
-    const int64_t m0 = tile / tiles_n * 32, n0 = tile % tiles_n * 32;
-    const int64_t m = min(m0 + r, p.M - 1), n = min(n0 + r, p.N - 1);  // rows past the end are read again
-    const uint8_t* pa = p.a + m * p.kb * 64 + 32 * g;
-    const uint8_t* pb = p.b + n * p.kb * 64 + 32 * g;
-    const uint8_t* psa = p.as + m * p.kb * 4;
-    const uint8_t* psb = p.bs + n * p.kb * 4;
-    v16f c = {};
-    for (int64_t k = 0; k < p.kb; ++k) {
-      const uint32_t sa = *(const uint32_t*)(psa + k * 4) >> (16 * g), sb = *(const uint32_t*)(psb + k * 4) >> (16 * g);
-      const v4u a0 = *(const v4u*)(pa + k * 64), a1 = *(const v4u*)(pa + k * 64 + 16);
-      const v4u b0 = *(const v4u*)(pb + k * 64), b1 = *(const v4u*)(pb + k * 64 + 16);
-      c = mfma_fp4_32<0>(b0, a0, c, sb, sa);
-      c = mfma_fp4_32<1>(b1, a1, c, sb, sa);
-    }
-    if (m0 + r >= p.M) continue;
+  __shared__ __align__(16) uint8_t turn[4][4096];
+  constexpr int D = KB ? KB : 1;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 31, g = lane >> 5;
+  for (int64_t tile = (int64_t)blockIdx.x * 4 + wave; tile < tiles; tile += (int64_t)gridDim.x * 4) {
+    const int64_t m0 = tile / tiles_n * 64, n0 = tile % tiles_n * 64;
+    v4u a[D][2][2], b[D][2][2];
+    uint32_t sa[D][2], sb[D][2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int64_t col = n0 + 8 * (i / 4) + 4 * g + i % 4;
-      if (col >= p.N) continue;
-      const int64_t at = (m0 + r) * p.ld + col;
-      if constexpr (BF16)
-        ((uint16_t*)p.out)[at] = f32_to_bf16(c[i]);
-      else
-        ((float*)p.out)[at] = p.accumulate ? ((float*)p.out)[at] + c[i] : c[i];
-    }
+    for (int k = 0; k < KB; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t m = min(m0 + 32 * i + r, p.M - 1), n = min(n0 + 32 * i + r, p.N - 1);  // rows past the end are read again
+        sa[k][i] = *(const uint16_t*)(p.as + (m * KB + k) * 4 + 2 * g);
+        sb[k][i] = *(const uint16_t*)(p.bs + (n * KB + k) * 4 + 2 * g);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          a[k][i][h] = *(const v4u*)(p.a + (m * KB + k) * 64 + 32 * g + 16 * h);
+          b[k][i][h] = *(const v4u*)(p.b + (n * KB + k) * 64 + 32 * g + 16 * h);
+        }
+      }
+    v16f c[2][2] = {};
+#pragma unroll
+    for (int k = 0; k < KB; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          c[i][j] = mfma_fp4_32<0>(b[k][j][0], a[k][i][0], c[i][j], sb[k][j], sa[k][i]);
+          c[i][j] = mfma_fp4_32<1>(b[k][j][1], a[k][i][1], c[i][j], sb[k][j], sa[k][i]);
+        }
+    // the matrix core's last results are written before they are read (and no
+    // product moves on to where its result is used)
+    asm volatile("s_nop 15\n\ts_nop 15" : "+a"(c[0][0]), "+a"(c[0][1]), "+a"(c[1][0]), "+a"(c[1][1])::"memory");
+    mx_write_tile<2, 2, BF16>(c, turn[wave], p.out, p.ld, p.accumulate, m0, n0, p.M, p.N);
   }
 }
 
@@ -747,6 +755,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx_few_kernel(MxMatmulArgs p) 
     }
   }
   // the matrix core's last results are written before they are read
+  __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_nop 15" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
   // lane: row r of a, columns 4 g .. +4
@@ -860,13 +869,18 @@ static hipError_t launch_mx_tile(const MxMatmulArgs& p, bool bf16, hipStream_t s
 static hipError_t launch_mx_matmul(const MxMatmulArgs& p, const MxPlan& plan, bool bf16, float* part, hipStream_t s) {
   if (mx_few_rows(p.M, p.N, p.K)) return launch_mx_few<0>(p, bf16, s);
   if (p.kb < 4) {
-    const int64_t tn = (p.N + 31) / 32, tiles = (p.M + 31) / 32 * tn, blocks = (tiles + 3) / 4;
+    const int64_t tn = (p.N + 63) / 64, tiles = (p.M + 63) / 64 * tn, blocks = (tiles + 3) / 4;
     const dim3 grid((unsigned)(blocks < kMxMaxGrid ? blocks : kMxMaxGrid));
-    if (bf16)
-      hipLaunchKernelGGL((mx_short_kernel<true>), grid, dim3(256), 0, s, p, tn, tiles);
-    else
-      hipLaunchKernelGGL((mx_short_kernel<false>), grid, dim3(256), 0, s, p, tn, tiles);
-    return hipGetLastError();
+    const auto run = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, p, tn, tiles);
+      return hipGetLastError();
+    };
+    switch (p.kb) {
+      case 0: return bf16 ? run(mx_short_kernel<0, true>) : run(mx_short_kernel<0, false>);
+      case 1: return bf16 ? run(mx_short_kernel<1, true>) : run(mx_short_kernel<1, false>);
+      case 2: return bf16 ? run(mx_short_kernel<2, true>) : run(mx_short_kernel<2, false>);
+      default: return bf16 ? run(mx_short_kernel<3, true>) : run(mx_short_kernel<3, false>);
+    }
   }
   MxMatmulArgs t = p;
   const bool split = plan.pieces > 1;
