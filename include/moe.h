@@ -460,8 +460,9 @@ moe_status_t moe_mxfp4_linear_bwd(int32_t M, int32_t N, int32_t K, const void* d
  *   seq_tokens int32 [num_seqs + 2]: the n_s, then N and S';
  *   lse f32 [T]: log sum_e exp(logits[t, e]), 0 for tokens that are not valid.
  * fp32 sums in a fixed order: repeated calls give the same bits.  ws: at least
- * moe_balance_bytes(T, E, num_seqs) bytes (0, and ws may be NULL, for up to 64
- * tokens; also 0 for invalid sizes).  A valid
+ * moe_balance_bytes(T, E, num_seqs) bytes (0, and ws may be NULL, for few
+ * tokens: up to 64 of at most 320 experts, 32 of 512, 16 of more; also 0 for
+ * invalid sizes).  A valid
  * token with a NaN or +inf logit makes the losses NaN.
  *
  * moe_router_bwd: d_logits f32 [T, E] (written whole; 0 for tokens that are

@@ -25,7 +25,6 @@
 
 namespace moe {
 
-constexpr int kBalChunk = 64;      // tokens per workgroup
 constexpr int kBalWaves = 16;
 constexpr int kBalGroups = 16;     // slot groups (waves) of the finishing workgroups
 constexpr int kBalMaxExperts = 1024;
@@ -33,7 +32,7 @@ constexpr int kBalMaxExperts = 1024;
 struct BalanceArgs {
   const float* logits;
   const int32_t* ids;
-  int32_t T, E, k, S, chunks;
+  int32_t T, E, k, S, chunk, chunks;  // chunk: tokens of a workgroup
   const uint8_t* mask;
   const int32_t* offsets;  // null: one sequence of all T rows
   float* lse;
@@ -177,13 +176,16 @@ __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Rows of a wave in flight together: bounded by registers.
+// Rows of a wave, all in registers together, by 64-expert columns per lane.
 constexpr int bal_rows(int vpl) { return vpl <= 5 ? 4 : vpl <= 8 ? 2 : 1; }
+// Tokens of a workgroup: one row set of its waves.
+constexpr int bal_chunk(int E) { return kBalWaves * bal_rows((E + 63) / 64); }
 
-// One workgroup per chunk of 64 tokens, one wave per token (four of them in
-// flight).  The chunk is walked sequence by sequence; each (chunk, sequence)
-// overlap leaves its sums in a slot of its own (c + s: along the rows every new
-// overlap raises c or s, so no two share a slot), added up in slot order by
+// One workgroup per chunk of tokens, one wave per token, U of them in flight:
+// the softmax of every row comes first, then the chunk is walked sequence by
+// sequence, adding up what is in registers.  Each (chunk, sequence) overlap
+// leaves its sums in a slot of its own (c + s: along the rows every new overlap
+// raises c or s, so no two share a slot), added up in slot order by
 // balance_finish_kernel.  ONE: the only chunk, which writes the results itself.
 template <int VPL, bool ONE>
 __global__ __launch_bounds__(64 * kBalWaves) void balance_chunk_kernel(BalanceArgs p) {
@@ -195,69 +197,85 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_chunk_kernel(BalanceAr
   __shared__ int32_t red_n[kBalWaves];
   __shared__ float red_l[kBalWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int c = blockIdx.x, tb = c * kBalChunk, te = min(p.T, tb + kBalChunk);
+  const int c = blockIdx.x, tb = c * kBalWaves * U, te = min(p.T, tb + kBalWaves * U);
   if (!ONE && c == 0 && tid == 0) *p.ticket = 0;
   if (ONE)
     for (int i = tid; i < p.S * p.E; i += 64 * kBalWaves) p.counts[i] = 0;
   if (ONE)
     for (int i = tid; i < p.S; i += 64 * kBalWaves) p.seq_tokens[i] = 0;
-  // rows outside every sequence
+  // (rows outside every sequence are not valid)
   const int first = min(max(seq_offset(p.offsets, p.T, 0), tb), te);
   const int last = min(max(seq_offset(p.offsets, p.T, p.S), first), te);
-  for (int t = tb + tid; t < te; t += 64 * kBalWaves)
-    if (t < first || t >= last) p.lse[t] = 0.0f;
+  float v[U][VPL], z[U];
+  int id[U];
+  bool ok[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int t = tb + wave + u * kBalWaves, in = max(min(t, te - 1), 0);
+    ok[u] = t >= first && t < last;
+    if (te > tb) {
+      load_row<VPL>(p.logits + (int64_t)in * p.E, p.E, v[u]);
+      id[u] = lane < p.k ? p.ids[(int64_t)in * p.k + lane] : -1;
+      if (p.mask) ok[u] = ok[u] && p.mask[in];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int t = tb + wave + u * kBalWaves;
+    float mx, sum, lse = 0.0f;
+    ok[u] = ok[u] && exp_row<VPL>(v[u], p.E, mx, sum);
+    if (ok[u]) {
+      const float inv = __builtin_amdgcn_rcpf(sum);
+      lse = mx + logf(sum);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) v[u][i] *= inv;
+    }
+    z[u] = lse * lse;
+    if (lane == 0 && t < te) p.lse[t] = lse;
+  }
   float one_loss = 0.0f, one_z = 0.0f;  // ONE, thread 0: sums over the sequences
   int one_n = 0, one_filled = 0;
-  int t0 = first;
+  int t0 = first, s0 = p.offsets && t0 < last ? seq_of(p.offsets, p.T, p.S, t0) : 0;
+  int end = seq_offset(p.offsets, p.T, min(s0 + lane, p.S - 1) + 1);  // lane's sequence s0 + lane
   while (t0 < last) {
-    const int s = p.offsets ? seq_of(p.offsets, p.T, p.S, t0) : 0;
-    if (s >= p.S) break;
-    const int t1 = max(min(seq_offset(p.offsets, p.T, s + 1), last), t0 + 1);
+    // the next sequence that ends after row t0
+    const uint64_t after = __ballot(s0 + lane < p.S && end > t0);
+    if (!after) {
+      s0 += 64;
+      if (s0 >= p.S) break;
+      end = seq_offset(p.offsets, p.T, min(s0 + lane, p.S - 1) + 1);
+      continue;
+    }
+    const int at = __builtin_ctzll(after), s = s0 + at;
+    const int t1 = min(__builtin_amdgcn_readlane(end, at), last);
     for (int e = tid; e < p.E; e += 64 * kBalWaves) hist[e] = 0;
     __syncthreads();
-    float acc[VPL] = {}, z = 0.0f;
+    float acc[VPL] = {}, zs = 0.0f;
     int n = 0;
-    for (int tw = t0 + wave; tw < t1; tw += U * kBalWaves) {
-      float v[U][VPL];
-      int id[U];
-      bool out[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = min(tw + u * kBalWaves, t1 - 1);
-        load_row<VPL>(p.logits + (int64_t)t * p.E, p.E, v[u]);
-        id[u] = lane < p.k ? p.ids[(int64_t)t * p.k + lane] : -1;
-        out[u] = p.mask && !p.mask[t];
-      }
+    for (int u = 0; u < U; ++u) {
+      const int t = tb + wave + u * kBalWaves;
+      if (ok[u] && t >= t0 && t < t1) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = tw + u * kBalWaves;
-        if (t >= t1) break;
-        float mx, sum, lse = 0.0f;
-        if (!out[u] && exp_row<VPL>(v[u], p.E, mx, sum)) {
-          const float inv = __builtin_amdgcn_rcpf(sum);
-          lse = mx + logf(sum);
-#pragma unroll
-          for (int i = 0; i < VPL; ++i) acc[i] += v[u][i] * inv;
-          z += lse * lse;
-          ++n;
-          if (id[u] >= 0 && id[u] < p.E) atomicAdd(&hist[id[u]], 1);
-        }
-        if (lane == 0) p.lse[t] = lse;
+        for (int i = 0; i < VPL; ++i) acc[i] += v[u][i];
+        zs += z[u];
+        ++n;
+        if (id[u] >= 0 && id[u] < p.E) atomicAdd(&hist[id[u]], 1);
       }
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       if (lane + 64 * i < p.E) red[wave * p.E + lane + 64 * i] = acc[i];
     if (lane == 0) {
-      red_z[wave] = z;
+      red_z[wave] = zs;
       red_n[wave] = n;
     }
     __syncthreads();
     int cnt = 0;
-    z = 0.0f;
+    zs = 0.0f;
 #pragma unroll
     for (int w = 0; w < kBalWaves; ++w) {
-      z += red_z[w];
+      zs += red_z[w];
       cnt += red_n[w];
     }
     const int64_t slot = c + s;
@@ -280,13 +298,13 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_chunk_kernel(BalanceAr
       __syncthreads();
       if (tid == 0) {
         for (int w = 0; w < kBalWaves; ++w) one_loss += red_l[w];
-        one_z += z;
+        one_z += zs;
         one_n += cnt;
         one_filled += cnt > 0;
         p.seq_tokens[s] = cnt;
       }
     } else if (tid == 0) {
-      p.pz[slot] = z;
+      p.pz[slot] = zs;
       p.pn[slot] = cnt;
     }
     __syncthreads();
@@ -311,7 +329,7 @@ __global__ __launch_bounds__(64 * kBalGroups) void balance_finish_kernel(Balance
   const int s = blockIdx.x / tiles, tile = blockIdx.x % tiles;
   const int e = tile * 64 + lane;
   const int lo = seq_offset(p.offsets, p.T, s), hi = seq_offset(p.offsets, p.T, s + 1);
-  const int c0 = lo / kBalChunk, c1 = lo < hi ? (hi - 1) / kBalChunk + 1 : c0;
+  const int c0 = lo / p.chunk, c1 = lo < hi ? (hi - 1) / p.chunk + 1 : c0;
   float sum = 0.0f;
   int cnt = 0;
   {
@@ -547,8 +565,8 @@ bool aligned4(const void* p) { return (uintptr_t)p % 4 == 0; }
 extern "C" {
 
 size_t moe_balance_bytes(int32_t T, int32_t E, int32_t num_seqs) {
-  if (!sizes_ok(T, E, 1, num_seqs) || T <= moe::kBalChunk) return 0;  // one workgroup keeps its sums to itself
-  const int64_t slots = (T + moe::kBalChunk - 1) / moe::kBalChunk + (int64_t)num_seqs;
+  if (!sizes_ok(T, E, 1, num_seqs) || T <= moe::bal_chunk(E)) return 0;  // one workgroup keeps its sums to itself
+  const int64_t slots = (T + moe::bal_chunk(E) - 1) / moe::bal_chunk(E) + (int64_t)num_seqs;
   return 2 * up256(slots * E * 4) + 2 * up256(slots * 4) + up256((int64_t)num_seqs * ((E + 63) / 64) * 4) +
          up256((int64_t)num_seqs * 4) + 256;
 }
@@ -571,7 +589,8 @@ moe_status_t moe_balance_loss(const float* logits, const int32_t* ids, int32_t T
   p.E = E;
   p.k = top_k;
   p.S = num_seqs;
-  p.chunks = T > 0 ? (T + moe::kBalChunk - 1) / moe::kBalChunk : 1;  // without tokens: zeros are written all the same
+  p.chunk = moe::bal_chunk(E);
+  p.chunks = T > 0 ? (T + p.chunk - 1) / p.chunk : 1;  // without tokens: zeros are written all the same
   p.mask = token_mask;
   p.offsets = seq_offsets;
   p.lse = lse;
@@ -579,7 +598,7 @@ moe_status_t moe_balance_loss(const float* logits, const int32_t* ids, int32_t T
   p.seq_tokens = seq_tokens;
   p.loss = loss;
   if (!need) return moe::launch_balance(p, (hipStream_t)stream) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
-  const int64_t slots = (T + moe::kBalChunk - 1) / moe::kBalChunk + (int64_t)num_seqs;
+  const int64_t slots = p.chunks + (int64_t)num_seqs;
   uint8_t* w = (uint8_t*)ws;
   p.psum = (float*)w; w += up256(slots * E * 4);
   p.pcount = (int32_t*)w; w += up256(slots * E * 4);
