@@ -187,6 +187,11 @@ constexpr int bal_chunk(int E) { return kBalWaves * bal_rows((E + 63) / 64); }
 // leaves its sums in a slot of its own (c + s: along the rows every new overlap
 // raises c or s, so no two share a slot), added up in slot order by
 // balance_finish_kernel.  ONE: the only chunk, which writes the results itself.
+//
+// 16384 tokens of 288 experts in 16 sequences: 11.9 us (19 MB at 1.6 TB/s: a
+// workgroup's loads, softmax and sums follow one another, and there is one
+// workgroup per compute unit), then 5.8 us to finish, both latency; chunks of
+// 32 tokens took 14.9 and 6.6 us.  64 tokens: 7.2 us in the one launch.
 template <int VPL, bool ONE>
 __global__ __launch_bounds__(64 * kBalWaves) void balance_chunk_kernel(BalanceArgs p) {
   constexpr int U = bal_rows(VPL);
@@ -445,8 +450,10 @@ struct RouterBwdArgs {
   float* d_logits;
 };
 
-// One wave per token.  The routing weights' part is scattered over a row of
-// LDS, one per wave.
+// One wave per token, everything it needs in flight at once.  The routing
+// weights' part is scattered over a row of LDS, one per wave.  16384 tokens of
+// 288 experts: 11.4 us, 40 MB at 3.5 TB/s, so near memory's rate; 64 tokens 3.8
+// us, a launch's latency.
 template <int VPL>
 __global__ __launch_bounds__(256) void router_bwd_kernel(RouterBwdArgs p) {
   __shared__ float scatter[4][64 * VPL];
