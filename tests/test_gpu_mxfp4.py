@@ -370,6 +370,49 @@ def test_repeated_runs_give_the_same_bits(M, m, n, k):
         assert all(torch.equal(o, want) for o in outs)
 
 
+@pytest.mark.parametrize("k", [400, 512, 600, 700, 900, 1100, 1200, 1700, 2048])
+def test_several_tiles_per_workgroup(M, k):
+    """More large tiles than compute units, whole and ragged ones, at lengths
+    that end anywhere in a group of four blocks: the same bits as products of
+    parts, which go through other tiles in the same order."""
+    m, n = 4900, 4700
+    a, sa, _ = _operand(m, k, 1)
+    b, sb, _ = _operand(n, k, 2)
+    for dtype in (BF16, F32):
+        out = torch.full((m, n + 4), 3.0, dtype=dtype, device="cuda")
+        M.moe_mxfp4_matmul(a, sa, b, sb, out=out[:, :n])
+        parts = [M.moe_mxfp4_matmul(a[i:i + 700], sa[i:i + 700], b, sb, out_dtype=dtype) for i in range(0, m, 700)]
+        assert torch.equal(out[:, :n], torch.cat(parts)) and (out[:, n:] == 3.0).all()
+    before = out.clone()
+    M.moe_mxfp4_matmul(a, sa, b, sb, out=out[:, :n], accumulate=True)
+    # fp32: the sum, rounded, added and rounded once more; of a sum with itself both are exact
+    assert torch.equal(out[:, :n], 2 * before[:, :n]) and (out[:, n:] == 3.0).all()
+
+
+@pytest.mark.parametrize("rows,k,n", [(1 << 24, 40, 33), (1 << 24, 520, 40), (70, 520, 1 << 24), (5, 130, 1 << 24), (66000, 512, 66000)])
+def test_largest_sides(M, rows, k, n):
+    """Sides of 2^24, and results past 2^32 elements: the first, some in the
+    middle and the last rows and columns as in products of those alone."""
+    def codes(r, seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        kp = (k + 127) // 128 * 128
+        q = torch.randint(0, 256, (r, kp // 2), generator=g, device="cuda", dtype=torch.uint8)
+        q[:, k // 2:] = 0
+        return q, torch.randint(118, 130, (r, kp // 32), generator=g, device="cuda", dtype=torch.uint8)
+
+    (a, sa), (b, sb) = codes(rows, 1), codes(n, 2)
+    out = M.moe_mxfp4_matmul(a, sa, b, sb)
+    pick = lambda size: [slice(i, min(i + 70, size)) for i in ({0, size // 2 - 3, size - 70} if size > 200 else {0})]
+    for i in pick(rows):
+        for j in pick(n):
+            want = M.moe_mxfp4_matmul(a[i].contiguous(), sa[i].contiguous(), b[j].contiguous(), sb[j].contiguous(), out_dtype=F32)
+            got = out[i, j].float()
+            # bf16 of the same sum, in an order of its own perhaps: half a step, and K roundings of the terms' size (<= 36 * 2^4 each)
+            assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + k * k * 36 * 16 * 2.0 ** -24).all()
+    del out, a, sa, b, sb
+    torch.cuda.empty_cache()
+
+
 def test_longest_sums(M):
     """K = 2^24, the longest: ones times ones with a power of two per row, sums
     that fp32 holds exactly; row offsets of up to 2 GB."""
