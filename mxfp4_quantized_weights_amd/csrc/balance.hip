@@ -188,10 +188,10 @@ constexpr int bal_chunk(int E) { return kBalWaves * bal_rows((E + 63) / 64); }
 // raises c or s, so no two share a slot), added up in slot order by
 // balance_finish_kernel.  ONE: the only chunk, which writes the results itself.
 //
-// 16384 tokens of 288 experts in 16 sequences: 11.9 us (19 MB at 1.6 TB/s: a
+// 16384 tokens of 288 experts in 16 sequences: 11.5 us (19 MB at 1.7 TB/s: a
 // workgroup's loads, softmax and sums follow one another, and there is one
 // workgroup per compute unit), then 5.8 us to finish, both latency; chunks of
-// 32 tokens took 14.9 and 6.6 us.  64 tokens: 7.2 us in the one launch.
+// 32 tokens took 14.9 and 6.6 us.  64 tokens: 6.9 us in the one launch.
 template <int VPL, bool ONE>
 __global__ __launch_bounds__(64 * kBalWaves) void balance_chunk_kernel(BalanceArgs p) {
   constexpr int U = bal_rows(VPL);
@@ -211,6 +211,10 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_chunk_kernel(BalanceAr
   // (rows outside every sequence are not valid)
   const int first = min(max(seq_offset(p.offsets, p.T, 0), tb), te);
   const int last = min(max(seq_offset(p.offsets, p.T, p.S), first), te);
+  // the sequences from s0 on, 64 at a time: the end of s0 + lane (found before
+  // the rows, whose loads it would otherwise wait for)
+  int s0 = p.S > 64 && first < last ? seq_of(p.offsets, p.T, p.S, first) : 0;
+  int end = seq_offset(p.offsets, p.T, min(s0 + lane, p.S - 1) + 1);
   float v[U][VPL], z[U];
   int id[U];
   bool ok[U];
@@ -240,8 +244,7 @@ __global__ __launch_bounds__(64 * kBalWaves) void balance_chunk_kernel(BalanceAr
   }
   float one_loss = 0.0f, one_z = 0.0f;  // ONE, thread 0: sums over the sequences
   int one_n = 0, one_filled = 0;
-  int t0 = first, s0 = p.offsets && t0 < last ? seq_of(p.offsets, p.T, p.S, t0) : 0;
-  int end = seq_offset(p.offsets, p.T, min(s0 + lane, p.S - 1) + 1);  // lane's sequence s0 + lane
+  int t0 = first;
   while (t0 < last) {
     // the next sequence that ends after row t0
     const uint64_t after = __ballot(s0 + lane < p.S && end > t0);

@@ -528,7 +528,9 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void mx_tile_kernel(MxMa
     mx_write_tile<MT, NT, BF16>(acc, lds + T::TURN + wave * 4096, out, p.ld, p.accumulate, mw, nw, p.M, p.N);
     if (!again) break;
     offsets();  // (not kept while the results are on their way out)
-    // stage 0 of the next tile; its other loads and the stores may still be under way
+    // stage 0 of the next tile; its other loads and the stores may still be under
+    // way (it has a stage 1: these tiles' sums are not split, and K has at least
+    // four blocks)
     constexpr int kLate = T::CHUNKS + kStores < 63 ? T::CHUNKS + kStores : 63;
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kLate) : "memory");
   }
@@ -853,7 +855,7 @@ static MxPlan mx_plan(int64_t M, int64_t N, int64_t kb) {
       best_tiles = tiles;
     }
   }
-  if (best_tiles <= 64 && kb >= 16) {
+  if (best_tiles <= 64 && best.t < 4 && kb >= 16) {
     int pieces = 1;
     while (pieces < 16 && best_tiles * pieces * 2 <= 256 && kb / (pieces * 2) >= 4) pieces *= 2;
     best.piece_kb = ((kb + pieces - 1) / pieces + 1) / 2 * 2;  // whole stages
