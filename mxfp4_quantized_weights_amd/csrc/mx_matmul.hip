@@ -822,13 +822,15 @@ static hipError_t launch_mx_few(const MxMatmulArgs& p, bool bf16, hipStream_t s)
 
 // The tile (64 t x 64 t, t = 4, 2 or 1) and the split of K for a product.
 //
-// Time per 128-wide half, in us, with c tiles per compute unit, from sweeps of
-// 22 products on one MI355X (M 16..16384, N 300..8192, K 1000..16384): a
-// 256-tile takes 0.95 for every full or partial round of c = 1; 128-tiles
-// max(0.44, 0.36 c); 64-tiles max(0.3, 0.15 c).  The least of the three picks
-// the tile that was fastest in all of them (4096 x 4096 x 1024: 16.3 / 17.7 /
-// 25.2 us; 2048 x 4096 x 4001: 32.7 / 26.6 / 44.4; 1024 x 2048 x 4096: - /
-// 18.2 / 15.5).
+// Time in us, fitted to a sweep of 23 products on one MI355X (M 700..16384, N
+// 1500..8192, K 512..4096), with c tiles per compute unit and K of kb blocks:
+// 256-tiles 3 + 6 and 0.78 kb for every full or partial round of c = 1;
+// 128-tiles 2.4 + 1.4 c + max(0.4, 0.26 c) kb; 64-tiles 3 + 0.4 c + max(0.2, 0.13
+// c) kb.  The least of the three is the fastest tile or within 3% of it in all
+// of them (256 / 128 / 64: 4096 x 4096 x 4096 35.0 / 41.6 / 70.7; 4900 x 4700 x
+// 520 41.7 / 28.7 / 33.9; 4900 x 4700 x 4096 69.0 / 66.4 / 106; 2048 x 4096 x 4001
+// 25.4 / 21.8 / 36.8; 1024 x 2048 x 4096 23.5 / 13.9 / 12.1; 1024 x 1024 x 1024
+// 10.2 / 5.3 / 4.4).
 //
 // A long sum over few tiles is split into pieces, up to one workgroup per
 // compute unit (128 x 2048 x 4096, 64 tiles: 11.3 us whole, 9.8 in 4 pieces;
@@ -847,8 +849,9 @@ static MxPlan mx_plan(int64_t M, int64_t N, int64_t kb) {
   for (int t : {4, 2, 1}) {
     const int64_t tiles = ((M + 64 * t - 1) / (64 * t)) * ((N + 64 * t - 1) / (64 * t));
     const double c = (double)tiles / kCus;
-    const double us = t == 4 ? 0.95 * (double)((tiles + 255) / 256) : t == 2 ? (c * 0.36 > 0.44 ? c * 0.36 : 0.44)
-                                                                            : (c * 0.15 > 0.3 ? c * 0.15 : 0.3);
+    const double us = t == 4   ? 3 + (double)((tiles + 255) / 256) * (6 + 0.78 * (double)kb)
+                      : t == 2 ? 2.4 + 1.4 * c + (c * 0.26 > 0.4 ? c * 0.26 : 0.4) * (double)kb
+                               : 3 + 0.4 * c + (c * 0.13 > 0.2 ? c * 0.13 : 0.2) * (double)kb;
     if (best_us == 0 || us < best_us) {
       best.t = t;
       best_us = us;

@@ -356,7 +356,7 @@ def test_products_past_32_bit_offsets(M):
     assert torch.equal(big[-100:, 2000:2200].cpu().double(), R.values(code, b)[:, :200])
 
 
-@pytest.mark.parametrize("m,n,k", [(2000, 2050, 1100), (3300, 3900, 600), (1000, 1000, 700), (4097, 4100, 520)])
+@pytest.mark.parametrize("m,n,k", [(2000, 2050, 1100), (3300, 3900, 600), (1000, 1000, 700), (4097, 4100, 520), (8100, 8100, 520)])
 def test_repeated_runs_give_the_same_bits(M, m, n, k):
     """Many runs one behind the other: a load that overtook a read of what it
     writes over would show in some of them."""
@@ -375,7 +375,7 @@ def test_several_tiles_per_workgroup(M, k):
     """More large tiles than compute units, whole and ragged ones, at lengths
     that end anywhere in a group of four blocks: the same bits as products of
     parts, which go through other tiles in the same order."""
-    m, n = 4900, 4700
+    m, n = 8100, 8100
     a, sa, _ = _operand(m, k, 1)
     b, sb, _ = _operand(n, k, 2)
     for dtype in (BF16, F32):
